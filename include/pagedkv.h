@@ -156,6 +156,42 @@ PKV_API int pkv_store_kvcache_rope(const void *q, void *q_out, const void *k, co
                                    int *dev_err, void *stream);
 
 /*
+ * store_kvcache_norm_rope: RMSNorm of every query and key head, then the
+ * rotation of pkv_store_kvcache_rope, then the store, in one pass: what a
+ * model with per-head query and key norms does between its QKV projection and
+ * its attention. For a q or k row x of one head, with its weight w:
+ *   n = x / sqrt(mean(x^2) + eps) * w
+ *   x'_i = n_i cos - n_j sin,  x'_j = n_j cos + n_i sin  for every pair (i, j)
+ * in binary32, rounded once: q' to bf16 in q_out, k' to bf16 or E4M3 in its
+ * slot (k' is not rounded to bf16 before E4M3; a per-token scale comes from
+ * the binary32 k'). v is stored as by pkv_store_kvcache.
+ *
+ *  q, k, v       bf16 [num_tokens][heads][head_dim]: a token's heads are
+ *                contiguous, tokens are *_stride elements apart (for example
+ *                one row of a fused QKV projection); q may be NULL (keys only)
+ *  q_out         bf16, tokens q_out_stride elements apart; may be q itself
+ *                with the same stride
+ *  q_weight, k_weight  [head_dim] bf16 (q_weight is ignored without q)
+ *  other arguments as pkv_store_kvcache_rope
+ *
+ * Slots of one call are distinct (apart from -1): of two rows for one slot
+ * either may stay, and parts of both.
+ *
+ * Host checks: as pkv_store_kvcache_rope, plus strides that are multiples of
+ * 8 elements and at least heads * head_dim, and eps >= 0 and finite. Device
+ * checks: as there (a token at a position outside the table is not written at
+ * all; slot -1 skips the cache write only).
+ */
+PKV_API int pkv_store_kvcache_norm_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                                        const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                        const void *q_weight, const void *k_weight, float eps, void *k_cache,
+                                        void *v_cache, const int32_t *slot_mapping, const int32_t *positions,
+                                        const float *cos_sin, int max_position, int rope_style, int num_tokens,
+                                        int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                        int64_t num_blocks, int cache_dtype, float *k_scale, float *v_scale,
+                                        int *dev_err, void *stream);
+
+/*
  * Split-K plan of a decode call. A sequence's tokens are cut into partitions
  * of partition_tokens logical tokens; each partition is one thread block per
  * KV head, and a reduce kernel merges the partials (flash-decoding). When
@@ -411,6 +447,103 @@ PKV_API int pkv_paged_attention_prefill(const void *q, const void *k_cache, cons
  */
 PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_blocks_per_seq,
                                            int block_size, int cache_dtype);
+
+/*
+ * pkv_paged_attention_tree: attention of drafted tokens over the paged cache,
+ * the verification pass of speculative decoding. Sequence i brings
+ * c_i = cu_q_lens[i + 1] - cu_q_lens[i] drafted tokens (rows cu_q_lens[i] .. of
+ * q), whose K/V a store has already written as the last c_i of its
+ * context_lens[i] positions, in the order of the rows. With
+ * base_i = context_lens[i] - c_i, a row attends to every position below base_i
+ * and to the drafts that its mask names:
+ *   out[row][h][:] = sum_t softmax_t(scale * q[row][h] . K_t) V_t
+ * over t < base_i and over t = base_i + u for the u with bit u of the row's
+ * mask set (the row itself only if its own bit is set). What a row does not
+ * attend to does not reach it, infinities and NaN included; a row that sees
+ * nothing (base_i = 0 and no bit) is zeros. Bits at and above c_i are ignored.
+ *
+ *  q              [total_q][num_q_heads][head_dim] bf16, contiguous
+ *  tree_mask      [total_q][mask_words] uint32: bit u % 32 of word u / 32
+ *  cu_q_lens      [num_seqs + 1] int32: 0, then running sums of the c_i
+ *  context_lens   [num_seqs] int32, c_i <= context_lens[i] <= max_context_len
+ *  max_q_len      host-known bound on every c_i, at most 32 * mask_words
+ *  max_context_len  host-known bound on every context, at most
+ *                 max_blocks_per_seq * block_size
+ *  partition_request, workspace  as for pkv_paged_attention_decode, with the
+ *                 plan of pkv_plan_tree (256-byte aligned; calls that may
+ *                 overlap on the GPU need separate workspaces)
+ *  out            [total_q][num_q_heads][head_dim] bf16; rows at and beyond
+ *                 cu_q_lens[num_seqs] are left as they are
+ *
+ * Scores and sums are binary32; see the kernel for the operand types. Host
+ * checks: as pkv_paged_attention_prefill (head_dim 64 or 128, group 1, 2, 4 or
+ * 8, block_size a power of two in [8, 1024], scale positive and finite), plus
+ * mask_words >= 1. Device checks: cu_q_lens that descends or leaves
+ * [0, total_q] (the sequence's rows stay as they are), a chunk longer than
+ * max_q_len or than its context, a context above max_context_len, or a block
+ * id outside the pool (the sequence's rows are zeros) set PKV_DEVERR_BOUNDS.
+ */
+PKV_API int pkv_plan_tree(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                          int max_q_len, int max_context_len, int cache_dtype, int partition_request,
+                          pkv_decode_plan *plan);
+PKV_API int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_cache,
+                                     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cu_q_lens,
+                                     const int32_t *context_lens, const uint32_t *tree_mask, int mask_words,
+                                     int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int block_size, int64_t num_blocks, float scale, int cache_dtype,
+                                     const float *k_scale, const float *v_scale, int max_q_len, int max_context_len,
+                                     int partition_request, void *workspace, size_t workspace_bytes, void *out,
+                                     int *dev_err, void *stream);
+
+/*
+ * pkv_compact_kvcache: after a tree's verification, the cached rows of the
+ * accepted drafts moved together. With c_i and base_i as for
+ * pkv_paged_attention_tree, the K and V rows (and per-token scales) of draft
+ * accepted[i][j] move to position base_i + j for j < num_accepted[i]; the
+ * sequence's context is then base_i + num_accepted[i]. Rows behind that are
+ * left as they are (each holds what it held, or a moved row's old copy).
+ *
+ *  accepted      [num_seqs][max_accepted] int32, in [0, c_i) and strictly
+ *                ascending over the first num_accepted[i]; the rest is not read
+ *  num_accepted  [num_seqs] int32, 0 <= n <= min(c_i, max_accepted)
+ *  k_scale, v_scale  the scale pools for PKV_CACHE_FP8_E4M3_TOKEN (moved with
+ *                the rows); ignored, and may be NULL, otherwise
+ *
+ * No two sequences of a call may hold their drafts in the same slots. Host
+ * checks: non-null pointers, 16-byte aligned caches, head_dim a multiple of 8,
+ * sizes >= 1 (num_seqs may be 0). Device checks: anything out of range (a
+ * length, a draft index, a list that does not ascend, a block id) sets
+ * PKV_DEVERR_BOUNDS and leaves that sequence's rows as they are.
+ */
+PKV_API int pkv_compact_kvcache(void *k_cache, void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                                const int32_t *cu_q_lens, const int32_t *context_lens, const int32_t *accepted,
+                                int max_accepted, const int32_t *num_accepted, int num_seqs, int num_kv_heads,
+                                int head_dim, int block_size, int64_t num_blocks, int cache_dtype, float *k_scale,
+                                float *v_scale, int *dev_err, void *stream);
+
+/*
+ * pkv_load_kvcache: cached rows read back as bf16, the inverse of the stores
+ * (for example to hand a request's cache to another worker). Output rows
+ * cu_rows[i] .. cu_rows[i + 1] - 1 of k_out and v_out are the tokens
+ * starts[i], starts[i] + 1, ... of sequence i (starts NULL: from token 0): a
+ * bf16 cache's rows as they are, E4M3 codes times their scale in binary32,
+ * rounded to bf16.
+ *
+ *  cu_rows       [num_seqs + 1] int32: 0, then running sums
+ *  k_out, v_out  [total_rows][num_kv_heads][head_dim] bf16; rows that belong to
+ *                no sequence (behind cu_rows[num_seqs]) are left as they are
+ *
+ * Host checks: non-null pointers, 16-byte aligned pools and outputs, head_dim
+ * a multiple of 8, sizes >= 1 (num_seqs and total_rows may be 0). Device
+ * checks: cu_rows that descends or leaves [0, total_rows], a token outside
+ * the table or a block id outside the pool (its rows are zeros) set
+ * PKV_DEVERR_BOUNDS.
+ */
+PKV_API int pkv_load_kvcache(const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *cu_rows, const int32_t *starts, int num_seqs,
+                             int total_rows, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                             int cache_dtype, const float *k_scale, const float *v_scale, void *k_out, void *v_out,
+                             int *dev_err, void *stream);
 
 /*
  * pkv_fused_add_rmsnorm: the residual add and RMSNorm around attention in

@@ -165,6 +165,67 @@ int pkv_store_kvcache_rope(const void *q, void *q_out, const void *k, const void
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+int pkv_store_kvcache_norm_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, const void *k,
+                                int64_t k_stride, const void *v, int64_t v_stride, const void *q_weight,
+                                const void *k_weight, float eps, void *k_cache, void *v_cache,
+                                const int32_t *slot_mapping, const int32_t *positions, const float *cos_sin,
+                                int max_position, int rope_style, int num_tokens, int num_q_heads, int num_kv_heads,
+                                int head_dim, int block_size, int64_t num_blocks, int cache_dtype, float *k_scale,
+                                float *v_scale, int *dev_err, void *stream) {
+    if (num_tokens < 0 || num_kv_heads < 1 || head_dim < 16 || head_dim % 16 != 0 || block_size < 1 ||
+        num_blocks < 1 || max_position < 1 || (rope_style != 0 && rope_style != 1))
+        return PKV_ERR_INVALID_ARG;
+    if (!valid_dtype(cache_dtype)) return PKV_ERR_INVALID_ARG;
+    // a row spans head_dim / 16 adjacent lanes (a power of two up to 32)
+    if (!pow2(head_dim / 16) || head_dim > 512) return PKV_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0f) || eps > 3.0e38f) return PKV_ERR_INVALID_ARG;  // negative, NaN or infinite
+    if ((q == nullptr) != (q_out == nullptr)) return PKV_ERR_INVALID_ARG;
+    if (q && num_q_heads < 1) return PKV_ERR_INVALID_ARG;
+    auto bad_stride = [&](int64_t stride, int heads) {
+        return stride % 8 != 0 || stride < (int64_t)heads * head_dim || stride > (INT64_MAX >> 34);
+    };
+    if (bad_stride(k_stride, num_kv_heads) || bad_stride(v_stride, num_kv_heads)) return PKV_ERR_INVALID_ARG;
+    if (q && (bad_stride(q_stride, num_q_heads) || bad_stride(q_out_stride, num_q_heads))) return PKV_ERR_INVALID_ARG;
+    const bool fp8 = cache_dtype != PKV_CACHE_BF16;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !k_weight || !k_cache || !v_cache || !slot_mapping || !positions || !cos_sin || (q && !q_weight))
+        return PKV_ERR_INVALID_ARG;
+    if (fp8 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_weight) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned16(cos_sin) || (q && (!aligned16(q) || !aligned16(q_out) || !aligned16(q_weight))))
+        return PKV_ERR_INVALID_ARG;
+    pkv::NormRopeArgs a;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_weight = static_cast<const __nv_bfloat16 *>(q_weight);
+    a.k_weight = static_cast<const __nv_bfloat16 *>(k_weight);
+    a.eps = eps;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.slots = slot_mapping;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.max_position = max_position;
+    a.num_tokens = num_tokens;
+    a.num_q_heads = q ? num_q_heads : 0;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.block_size = block_size;
+    a.pool_slots = (long long)num_blocks * block_size;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.dev_err = dev_err;
+    cudaError_t e =
+        pkv::launch_store_norm_rope(a, rope_style, cache_dtype, num_sms(), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 int pkv_plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                     int max_context_len, int cache_dtype, int partition_request, pkv_decode_plan *plan) {
     if (!plan) return PKV_ERR_INVALID_ARG;
@@ -408,6 +469,173 @@ int pkv_paged_attention_prefill(const void *q, const void *k_cache, const void *
     }
     cudaError_t e = pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
     if (e == cudaErrorInvalidConfiguration) return PKV_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+namespace {
+
+int check_tree_shape(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_q_len,
+                     int max_context_len, int cache_dtype) {
+    if (num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || max_q_len < 1 || max_context_len < 1)
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    if (!valid_dtype(cache_dtype)) return PKV_ERR_INVALID_ARG;
+    if (!pow2(block_size) || block_size < 8 || block_size > 1024) return PKV_ERR_INVALID_ARG;
+    if (!pkv::prefill_supported(head_dim, num_q_heads / num_kv_heads)) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+}  // namespace
+
+int pkv_plan_tree(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_q_len,
+                  int max_context_len, int cache_dtype, int partition_request, pkv_decode_plan *plan) {
+    if (!plan) return PKV_ERR_INVALID_ARG;
+    const int st = check_tree_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len,
+                                    max_context_len, cache_dtype);
+    if (st != PKV_OK) return st;
+    if (partition_request < -1) return PKV_ERR_INVALID_ARG;
+    plan->partition_tokens = 0;
+    plan->max_partitions = 1;
+    plan->workspace_bytes = 0;
+    return PKV_OK;
+}
+
+int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *cu_q_lens, const int32_t *context_lens,
+                             const uint32_t *tree_mask, int mask_words, int num_seqs, int total_q, int num_q_heads,
+                             int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+                             int cache_dtype, const float *k_scale, const float *v_scale, int max_q_len,
+                             int max_context_len, int partition_request, void *workspace, size_t workspace_bytes,
+                             void *out, int *dev_err, void *stream) {
+    pkv_decode_plan plan;
+    const int st = pkv_plan_tree(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len,
+                                 max_context_len, cache_dtype, partition_request, &plan);
+    if (st != PKV_OK) return st;
+    if (total_q < 0 || mask_words < 1 || (long long)mask_words * 32 < max_q_len) return PKV_ERR_INVALID_ARG;
+    if (!q || !k_cache || !v_cache || !block_tables || !cu_q_lens || !context_lens || !tree_mask || !out)
+        return PKV_ERR_INVALID_ARG;
+    if (cache_dtype != PKV_CACHE_BF16 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
+    if (max_blocks_per_seq < 1 || num_blocks < 1 || num_blocks > INT32_MAX) return PKV_ERR_INVALID_ARG;
+    if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size) return PKV_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || scale > 3.0e38f) return PKV_ERR_INVALID_ARG;  // positive and finite
+    if (plan.workspace_bytes > 0) {
+        if (!workspace || workspace_bytes < plan.workspace_bytes) return PKV_ERR_WORKSPACE;
+        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_ERR_INVALID_ARG;
+    }
+    if (num_seqs == 0 || total_q == 0) return PKV_OK;
+    pkv::TreeArgs a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_tables = block_tables;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.cu_q_lens = cu_q_lens;
+    a.context_lens = context_lens;
+    a.mask = tree_mask;
+    a.mask_words = mask_words;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.scale = scale;
+    a.mode = cache_dtype;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.max_q_len = max_q_len;
+    a.max_context_len = max_context_len;
+    a.partition_tokens = plan.partition_tokens;
+    a.num_partitions = plan.max_partitions;
+    a.part_o = nullptr;
+    a.part_ml = nullptr;
+    if (plan.workspace_bytes > 0) {
+        const size_t rows = (size_t)total_q * num_q_heads * plan.max_partitions;
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                              round_up(rows * head_dim * sizeof(float), 256));
+    }
+    a.out = out;
+    a.dev_err = dev_err;
+    cudaError_t e = pkv::launch_tree(a, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorInvalidConfiguration) return PKV_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int pkv_compact_kvcache(void *k_cache, void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                        const int32_t *cu_q_lens, const int32_t *context_lens, const int32_t *accepted,
+                        int max_accepted, const int32_t *num_accepted, int num_seqs, int num_kv_heads, int head_dim,
+                        int block_size, int64_t num_blocks, int cache_dtype, float *k_scale, float *v_scale,
+                        int *dev_err, void *stream) {
+    if (num_seqs < 0 || num_kv_heads < 1 || head_dim < 8 || head_dim % 8 != 0 || block_size < 1 || num_blocks < 1 ||
+        max_blocks_per_seq < 1 || max_accepted < 1)
+        return PKV_ERR_INVALID_ARG;
+    if (!valid_dtype(cache_dtype)) return PKV_ERR_INVALID_ARG;
+    if (num_blocks > INT32_MAX || head_dim > (1 << 20)) return PKV_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !block_tables || !cu_q_lens || !context_lens || !accepted || !num_accepted)
+        return PKV_ERR_INVALID_ARG;
+    const bool token = cache_dtype == PKV_CACHE_FP8_E4M3_TOKEN;
+    if (token && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
+    pkv::CompactArgs a;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = token ? k_scale : nullptr;
+    a.v_scale = token ? v_scale : nullptr;
+    a.block_tables = block_tables;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.cu_q_lens = cu_q_lens;
+    a.context_lens = context_lens;
+    a.accepted = accepted;
+    a.max_accepted = max_accepted;
+    a.num_accepted = num_accepted;
+    a.num_seqs = num_seqs;
+    a.num_kv_heads = num_kv_heads;
+    a.row_bytes = head_dim * (cache_dtype == PKV_CACHE_BF16 ? 2 : 1);
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.dev_err = dev_err;
+    cudaError_t e = pkv::launch_compact(a, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorInvalidConfiguration) return PKV_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int pkv_load_kvcache(const void *k_cache, const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *cu_rows, const int32_t *starts, int num_seqs, int total_rows, int num_kv_heads,
+                     int head_dim, int block_size, int64_t num_blocks, int cache_dtype, const float *k_scale,
+                     const float *v_scale, void *k_out, void *v_out, int *dev_err, void *stream) {
+    if (num_seqs < 0 || total_rows < 0 || num_kv_heads < 1 || head_dim < 8 || head_dim % 8 != 0 || block_size < 1 ||
+        num_blocks < 1 || max_blocks_per_seq < 1)
+        return PKV_ERR_INVALID_ARG;
+    if (!valid_dtype(cache_dtype)) return PKV_ERR_INVALID_ARG;
+    if (num_blocks > INT32_MAX || head_dim > (1 << 20)) return PKV_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_rows == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !block_tables || !cu_rows || !k_out || !v_out) return PKV_ERR_INVALID_ARG;
+    if (cache_dtype != PKV_CACHE_BF16 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+        return PKV_ERR_INVALID_ARG;
+    pkv::LoadArgs a;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_tables = block_tables;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.cu_rows = cu_rows;
+    a.starts = starts;
+    a.num_seqs = num_seqs;
+    a.total_rows = total_rows;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.k_out = static_cast<uint4 *>(k_out);
+    a.v_out = static_cast<uint4 *>(v_out);
+    a.dev_err = dev_err;
+    cudaError_t e = pkv::launch_load(a, cache_dtype, num_sms(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

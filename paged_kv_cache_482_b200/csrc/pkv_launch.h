@@ -1,6 +1,7 @@
 // pkv_launch.h -- internal launchers behind the C ABI (not installed).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -147,6 +148,113 @@ struct NormArgs {
 
 int norm_max_hidden();
 cudaError_t launch_fused_add_rmsnorm(const NormArgs &a, int num_sms, cudaStream_t stream);
+
+// Per-head RMSNorm + RoPE + store (norm_rope.cu).
+struct NormRopeArgs {
+    const __nv_bfloat16 *q;  // null with num_q_heads 0: keys only
+    __nv_bfloat16 *q_out;
+    const __nv_bfloat16 *k;
+    const __nv_bfloat16 *v;
+    long long q_stride;  // elements between tokens
+    long long q_out_stride;
+    long long k_stride;
+    long long v_stride;
+    const __nv_bfloat16 *q_weight;
+    const __nv_bfloat16 *k_weight;
+    float eps;
+    void *k_cache;
+    void *v_cache;
+    const int32_t *slots;
+    const int32_t *positions;
+    const float *cos_sin;
+    int max_position;
+    int num_tokens;
+    int num_q_heads;
+    int num_kv_heads;
+    int head_dim;
+    int block_size;
+    long long pool_slots;
+    float *k_scale;
+    float *v_scale;
+    int *dev_err;
+};
+cudaError_t launch_store_norm_rope(const NormRopeArgs &a, int style, int mode, int num_sms, cudaStream_t stream);
+
+// Rows of accepted drafts closed up, and cached rows read back (move_kvcache.cu).
+struct CompactArgs {
+    void *k_cache;
+    void *v_cache;
+    float *k_scale;  // scale pools, or null
+    float *v_scale;
+    const int32_t *block_tables;
+    int max_blocks_per_seq;
+    const int32_t *cu_q_lens;
+    const int32_t *context_lens;
+    const int32_t *accepted;
+    int max_accepted;
+    const int32_t *num_accepted;
+    int num_seqs;
+    int num_kv_heads;
+    int row_bytes;
+    int block_size;
+    long long num_blocks;
+    int *dev_err;
+};
+cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream);
+
+struct LoadArgs {
+    const void *k_cache;
+    const void *v_cache;
+    const float *k_scale;
+    const float *v_scale;
+    const int32_t *block_tables;
+    int max_blocks_per_seq;
+    const int32_t *cu_rows;
+    const int32_t *starts;  // may be null
+    int num_seqs;
+    int total_rows;
+    int num_kv_heads;
+    int head_dim;
+    int block_size;
+    long long num_blocks;
+    uint4 *k_out;
+    uint4 *v_out;
+    int *dev_err;
+};
+cudaError_t launch_load(const LoadArgs &a, int mode, int num_sms, cudaStream_t stream);
+
+// Attention of drafted trees (tree.cu).
+struct TreeArgs {
+    const void *q;
+    const void *k_cache;
+    const void *v_cache;
+    const int32_t *block_tables;
+    int max_blocks_per_seq;
+    const int32_t *cu_q_lens;
+    const int32_t *context_lens;
+    const uint32_t *mask;  // [total_q][mask_words]
+    int mask_words;
+    int num_seqs;
+    int total_q;
+    int num_q_heads;
+    int num_kv_heads;
+    int head_dim;
+    int block_size;
+    long long num_blocks;
+    float scale;
+    int mode;  // 0 bf16, 1 E4M3 with a scale per KV head, 2 with one per row
+    const float *k_scale;
+    const float *v_scale;
+    int max_q_len;
+    int max_context_len;
+    int partition_tokens;  // 0: one partition
+    int num_partitions;
+    float *part_o;
+    float *part_ml;
+    void *out;
+    int *dev_err;
+};
+cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream);
 
 bool prefill_supported(int head_dim, int group);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);

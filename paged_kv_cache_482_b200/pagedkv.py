@@ -9,6 +9,7 @@ The functions mirror ``include/pagedkv.h``:
 
 * ``store_kvcache`` -- ``pkv_store_kvcache``
 * ``store_kvcache_rope`` -- ``pkv_store_kvcache_rope``
+* ``store_kvcache_norm_rope`` -- ``pkv_store_kvcache_norm_rope``
 * ``plan_decode`` -- ``pkv_plan_decode``
 * ``decode_workspace_bytes`` -- ``pkv_decode_workspace_bytes``
 * ``paged_attention_decode`` -- ``pkv_paged_attention_decode``
@@ -16,6 +17,9 @@ The functions mirror ``include/pagedkv.h``:
   ``pkv_plan_decode_shared_prefix`` / ``pkv_paged_attention_decode_shared_prefix``
 * ``paged_attention_prefill`` -- ``pkv_paged_attention_prefill``
 * ``prefill_workspace_bytes`` -- ``pkv_prefill_workspace_bytes``
+* ``plan_tree`` / ``paged_attention_tree`` -- ``pkv_plan_tree`` / ``pkv_paged_attention_tree``
+* ``compact_kvcache`` -- ``pkv_compact_kvcache``
+* ``load_kvcache`` -- ``pkv_load_kvcache``
 * ``fused_add_rmsnorm`` -- ``pkv_fused_add_rmsnorm``
 * ``read_device_error`` -- ``pkv_read_device_error``
 """
@@ -47,7 +51,8 @@ EXPORTED = ("pkv_store_kvcache", "pkv_store_kvcache_rope", "pkv_plan_decode", "p
             "pkv_plan_decode_shared_prefix", "pkv_paged_attention_decode_shared_prefix",
             "pkv_paged_attention_decode", "pkv_status_string", "pkv_read_device_error", "pkv_version",
             "pkv_paged_attention_decode_static_scratch", "pkv_paged_attention_prefill",
-            "pkv_prefill_workspace_bytes", "pkv_fused_add_rmsnorm")
+            "pkv_prefill_workspace_bytes", "pkv_fused_add_rmsnorm", "pkv_store_kvcache_norm_rope", "pkv_plan_tree",
+            "pkv_paged_attention_tree", "pkv_compact_kvcache", "pkv_load_kvcache")
 
 
 class PagedKVError(RuntimeError):
@@ -112,6 +117,18 @@ def load_library(path: str):
     L.pkv_prefill_workspace_bytes.restype = sz
     L.pkv_fused_add_rmsnorm.argtypes = [vp, vp, vp, vp, i32, i32, f32, vp]
     L.pkv_fused_add_rmsnorm.restype = i32
+    L.pkv_store_kvcache_norm_rope.argtypes = ([vp, i64] * 4 + [vp, vp, f32] + [vp] * 5 + [i32] * 7
+                                              + [i64, i32, vp, vp, vp, vp])
+    L.pkv_store_kvcache_norm_rope.restype = i32
+    L.pkv_plan_tree.argtypes = [i32] * 9 + [c.POINTER(_Plan)]
+    L.pkv_plan_tree.restype = i32
+    L.pkv_paged_attention_tree.argtypes = ([vp] * 4 + [i32, vp, vp, vp] + [i32] * 7 + [i64, f32, i32, vp, vp, i32, i32,
+                                                                                      i32, vp, sz, vp, vp, vp])
+    L.pkv_paged_attention_tree.restype = i32
+    L.pkv_compact_kvcache.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, i32, i64, i32, vp, vp, vp, vp]
+    L.pkv_compact_kvcache.restype = i32
+    L.pkv_load_kvcache.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp]
+    L.pkv_load_kvcache.restype = i32
     if hasattr(L, "pkv_paged_attention_decode_static_scratch"):
         L.pkv_paged_attention_decode_static_scratch.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32,
                                                                 i32, i64, f32, i32, vp, vp, i32, i32, vp, vp, vp]
@@ -147,6 +164,76 @@ def _cache_dtype(t: torch.Tensor, k_scale=None) -> int:
             return PKV_CACHE_FP8_E4M3_TOKEN
         return PKV_CACHE_FP8_E4M3
     raise TypeError(f"KV pool dtype {t.dtype}: expected bfloat16 or an 8-bit E4M3 container")
+
+
+def cache_dtype(k_cache: torch.Tensor, k_scale=None) -> int:
+    """The ``PKV_CACHE_*`` value of a pool and its scales."""
+    return _cache_dtype(k_cache, k_scale)
+
+
+def _pool_args(k_cache, v_cache, k_scale, v_scale) -> int:
+    """Check a pool pair and its scales; returns the cache type."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("the pools must be two [num_blocks, num_kv_heads, block_size, head_dim] tensors of one type")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the pools must be contiguous")
+    dt = _cache_dtype(k_cache, k_scale)
+    if dt != PKV_CACHE_BF16:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an E4M3 cache needs k_scale and v_scale")
+        shape = k_cache.shape[1:2] if dt == PKV_CACHE_FP8_E4M3 else k_cache.shape[:3]
+        for t in (k_scale, v_scale):
+            if t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError("scales must be contiguous fp32 [num_kv_heads], or scale pools [num_blocks, "
+                                 "num_kv_heads, block_size], both of one kind")
+    return dt
+
+
+def _i32(t, name, shape):
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous int32")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _on_device(*tensors) -> torch.device:
+    """The one CUDA device that holds every given tensor."""
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("the tensors must be on one CUDA device")
+    return dev
+
+
+def _torch_stream(stream, dev):
+    """``stream`` (torch stream, raw handle or None: the device's current one) as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
+
+
+def _empty(shape, dtype, dev, stream):
+    """A new tensor whose memory belongs to ``stream``, where the kernels use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(_torch_stream(stream, dev)):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(fn, where, dev, stream, *args):
+    """Call a launching entry point with ``dev`` current and the stream last."""
+    handle = _torch_stream(stream, dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, handle), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, handle), where)
 
 
 def _check(status: int, where: str):
@@ -204,6 +291,65 @@ def store_kvcache_rope(k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
                                       nq, nkv, d, bs, nblk, _cache_dtype(k_cache, k_scale), _ptr(k_scale),
                                       _ptr(v_scale), _ptr(dev_err), _stream(stream))
     _check(st, "pkv_store_kvcache_rope")
+    return q_out
+
+
+def _heads(t, name, N, d):
+    """Token stride of a bf16 [N, heads, d] tensor whose heads are contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != d:
+        raise ValueError(f"{name} must be [N, heads, head_dim]")
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and t.shape[1] > 1):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return sn if N > 1 else t.shape[1] * d  # the stride of a single token is never used
+
+
+def store_kvcache_norm_rope(k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, k_weight, eps, q=None,
+                            q_weight=None, q_out=None, style=0, k_scale=None, v_scale=None, dev_err=None, stream=None):
+    """RMSNorm over head_dim of every head of k (weight ``k_weight [d]`` bf16)
+    and of q (``q_weight``), rotation as in ``store_kvcache_rope``, then the
+    store of the normed, rotated k and of v. k, v, q (and q_out) are
+    ``[N, heads, d]`` bf16 whose tokens may lie any multiple of 8 elements apart:
+    views of a fused projection's output need no copy. Slots other than -1 must
+    be distinct. Returns ``q_out`` (allocated when q is given without it)."""
+    dt = _pool_args(k_cache, v_cache, k_scale, v_scale)
+    nblk, nkv, bs, d = k_cache.shape
+    N = k.shape[0]
+    k_stride, v_stride = _heads(k, "k", N, d), _heads(v, "v", N, d)
+    if k.shape[1] != nkv or v.shape[1] != nkv:
+        raise ValueError("k and v must have the pools' KV heads")
+    _i32(slot_mapping, "slot_mapping", (N,))
+    _i32(positions, "positions", (N,))
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise TypeError("cos_sin must be a contiguous fp32 [max_position, head_dim] table")
+    if cos_sin.shape[1] != d:
+        raise ValueError("cos_sin does not match head_dim")
+    nq = q_stride = out_stride = 0
+    if q is not None:
+        q_stride = _heads(q, "q", N, d)
+        nq = q.shape[1]
+        if q_weight is None:
+            raise ValueError("q needs q_weight")
+        if q_out is not None:
+            out_stride = _heads(q_out, "q_out", N, d)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must be shaped like q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    for w in (k_weight, q_weight):
+        if w is not None and (w.dtype != torch.bfloat16 or w.shape != (d,) or not w.is_contiguous()):
+            raise TypeError("the norm weights must be contiguous bfloat16 [head_dim]")
+    dev = _on_device(k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, k_weight, q, q_weight, q_out, k_scale,
+                     v_scale, dev_err)
+    if q is not None and q_out is None:
+        q_out = _empty(q.shape, torch.bfloat16, dev, stream)
+        out_stride = nq * d
+    _run(lib().pkv_store_kvcache_norm_rope, "pkv_store_kvcache_norm_rope", dev, stream, _addr(q), q_stride,
+         _addr(q_out), out_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, _addr(q_weight), _addr(k_weight),
+         eps, _addr(k_cache), _addr(v_cache), _addr(slot_mapping), _addr(positions), _addr(cos_sin), cos_sin.shape[0],
+         style, N, nq, nkv, d, bs, nblk, dt, _addr(k_scale), _addr(v_scale), _addr(dev_err))
     return q_out
 
 
@@ -395,6 +541,141 @@ def paged_attention_prefill(q, k_cache, v_cache, block_tables, cu_q_lens, contex
         _ptr(v_scale), int(max_q_len), _ptr(workspace), ws_bytes, _ptr(out), _ptr(dev_err), _stream(stream))
     _check(st, "pkv_paged_attention_prefill")
     return out
+
+
+def tree_mask(parents, words=None):
+    """Host helper for ``paged_attention_tree``: the masks of one sequence's
+    drafts from their parents (``parents[j] < j``; -1: the draft follows the
+    last cached token). Every draft sees itself and its ancestors. Returns
+    (mask ``[c, words]`` int32, depth ``[c]`` int32) on the CPU; a draft's
+    position is the number of cached tokens before the drafts plus its depth."""
+    parents = [int(p) for p in parents]
+    words = words or max(1, -(-len(parents) // 32))
+    if len(parents) > 32 * words:
+        raise ValueError("words is too small for the drafts")
+    sees, depth = [], []
+    for j, p in enumerate(parents):
+        if not -1 <= p < j:
+            raise ValueError("a draft's parent must be -1 or an earlier draft")
+        sees.append((sees[p] if p >= 0 else 0) | (1 << j))
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+    bits = np.array([[(m >> (32 * w)) & 0xFFFFFFFF for w in range(words)] for m in sees], dtype=np.uint32)
+    return torch.from_numpy(bits.reshape(-1, words).view(np.int32)), torch.tensor(depth, dtype=torch.int32)
+
+
+def plan_tree(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_context_len,
+              cache_dtype=PKV_CACHE_BF16, partition_request=0) -> dict:
+    """The split plan and workspace size of a ``paged_attention_tree`` call of these sizes."""
+    plan = _Plan()
+    st = lib().pkv_plan_tree(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_context_len,
+                             int(cache_dtype), partition_request, ctypes.byref(plan))
+    _check(st, "pkv_plan_tree")
+    return dict(partition_tokens=plan.partition_tokens, max_partitions=plan.max_partitions,
+                workspace_bytes=plan.workspace_bytes)
+
+
+def paged_attention_tree(q, k_cache, v_cache, block_tables, cu_q_lens, context_lens, tree_mask, scale, max_q_len,
+                         out=None, k_scale=None, v_scale=None, max_context_len=None, partition_request=0,
+                         workspace=None, dev_err=None, stream=None):
+    """Attention of drafted trees over the paged cache: the drafts of sequence
+    i (rows ``cu_q_lens[i]`` .. ``cu_q_lens[i+1] - 1`` of ``q``, ``[total_q,
+    nq, d]`` bf16) are the last of its ``context_lens[i]`` cached tokens; a row
+    attends to every token before them and to the drafts whose bits are set in
+    its row of ``tree_mask`` (``[total_q, words]`` int32, see ``tree_mask()``).
+    A row that sees nothing is zeros. ``max_q_len`` and ``max_context_len``
+    (default: the block table's capacity) are host-known bounds. A workspace is
+    allocated when the plan (``plan_tree``) needs one and none is given; calls
+    that may overlap need workspaces of their own."""
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+        raise TypeError("q must be contiguous bfloat16 [total_q, heads, head_dim]")
+    dt = _pool_args(k_cache, v_cache, k_scale, v_scale)
+    T, nq, d = q.shape
+    nblk, nkv, bs, d2 = k_cache.shape
+    if d2 != d:
+        raise ValueError("q and the pools disagree on head_dim")
+    S = context_lens.shape[0]
+    _i32(context_lens, "context_lens", (S,))
+    _i32(cu_q_lens, "cu_q_lens", (S + 1,))
+    maxb = block_tables.shape[1]
+    _i32(block_tables, "block_tables", (S, maxb))
+    words = tree_mask.shape[1]
+    _i32(tree_mask, "tree_mask", (T, words))
+    if max_context_len is None:
+        max_context_len = maxb * bs
+    if out is not None and (out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous()):
+        raise ValueError("out must be contiguous bfloat16 shaped like q")
+    dev = _on_device(q, k_cache, v_cache, block_tables, cu_q_lens, context_lens, tree_mask, out, k_scale, v_scale,
+                     workspace, dev_err)
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
+    if workspace is None:
+        need = plan_tree(S, nq, nkv, d, bs, max_q_len, max_context_len, dt, partition_request)["workspace_bytes"]
+        if need:
+            workspace = _empty(need, torch.uint8, dev, stream)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _run(lib().pkv_paged_attention_tree, "pkv_paged_attention_tree", dev, stream, _addr(q), _addr(k_cache),
+         _addr(v_cache), _addr(block_tables), maxb, _addr(cu_q_lens), _addr(context_lens), _addr(tree_mask), words, S,
+         T, nq, nkv, d, bs, nblk, scale, dt, _addr(k_scale), _addr(v_scale), max_q_len, max_context_len,
+         partition_request, _addr(workspace), ws_bytes, _addr(out), _addr(dev_err))
+    return out
+
+
+def compact_kvcache(k_cache, v_cache, block_tables, cu_q_lens, context_lens, accepted, num_accepted, k_scale=None,
+                    v_scale=None, dev_err=None, stream=None):
+    """After a tree's verification: the cached rows of the accepted drafts
+    (``accepted[i, :num_accepted[i]]``, ascending draft indices of sequence i;
+    ``accepted`` ``[S, max_accepted]`` int32) move, in place, to the first
+    places behind the tokens that precede the drafts. ``cu_q_lens`` and
+    ``context_lens`` are those of the ``paged_attention_tree`` call; the new
+    context of sequence i is ``context_lens[i]`` minus its drafts plus
+    ``num_accepted[i]``."""
+    dt = _pool_args(k_cache, v_cache, k_scale, v_scale)
+    nblk, nkv, bs, d = k_cache.shape
+    S = context_lens.shape[0]
+    _i32(context_lens, "context_lens", (S,))
+    _i32(cu_q_lens, "cu_q_lens", (S + 1,))
+    _i32(num_accepted, "num_accepted", (S,))
+    maxb, most = block_tables.shape[1], accepted.shape[1]
+    _i32(block_tables, "block_tables", (S, maxb))
+    _i32(accepted, "accepted", (S, most))
+    dev = _on_device(k_cache, v_cache, block_tables, cu_q_lens, context_lens, accepted, num_accepted, k_scale, v_scale,
+                     dev_err)
+    _run(lib().pkv_compact_kvcache, "pkv_compact_kvcache", dev, stream, _addr(k_cache), _addr(v_cache),
+         _addr(block_tables), maxb, _addr(cu_q_lens), _addr(context_lens), _addr(accepted), most, _addr(num_accepted),
+         S, nkv, d, bs, nblk, dt, _addr(k_scale), _addr(v_scale), _addr(dev_err))
+
+
+def load_kvcache(k_cache, v_cache, block_tables, cu_rows, total_rows=None, starts=None, k_out=None, v_out=None,
+                 k_scale=None, v_scale=None, dev_err=None, stream=None):
+    """Read cached rows back as bf16: rows ``cu_rows[i]`` .. ``cu_rows[i+1] - 1``
+    of the result are tokens ``starts[i]``, ``starts[i] + 1``, ... of sequence i
+    (``starts`` None: from token 0). Give ``k_out`` and ``v_out`` ``[total_rows,
+    nkv, d]`` bf16, or ``total_rows`` to have them allocated (rows of no
+    sequence are left as they are). Returns (k, v)."""
+    dt = _pool_args(k_cache, v_cache, k_scale, v_scale)
+    nblk, nkv, bs, d = k_cache.shape
+    S, maxb = block_tables.shape
+    _i32(block_tables, "block_tables", (S, maxb))
+    _i32(cu_rows, "cu_rows", (S + 1,))
+    if starts is not None:
+        _i32(starts, "starts", (S,))
+    if (k_out is None) != (v_out is None) or (k_out is None and total_rows is None):
+        raise ValueError("give both outputs, or total_rows")
+    if k_out is not None:
+        T = k_out.shape[0]
+        for t in (k_out, v_out):
+            if t.dtype != torch.bfloat16 or t.shape != (T, nkv, d) or not t.is_contiguous():
+                raise ValueError("k_out and v_out must be contiguous bfloat16 [total_rows, num_kv_heads, head_dim]")
+        if total_rows is not None and total_rows != T:
+            raise ValueError("total_rows is not the outputs'")
+    dev = _on_device(k_cache, v_cache, block_tables, cu_rows, starts, k_out, v_out, k_scale, v_scale, dev_err)
+    if k_out is None:
+        T = int(total_rows)
+        k_out, v_out = (_empty((T, nkv, d), torch.bfloat16, dev, stream) for _ in range(2))
+    _run(lib().pkv_load_kvcache, "pkv_load_kvcache", dev, stream, _addr(k_cache), _addr(v_cache), _addr(block_tables),
+         maxb, _addr(cu_rows), _addr(starts), S, T, nkv, d, bs, nblk, dt, _addr(k_scale), _addr(v_scale),
+         _addr(k_out), _addr(v_out), _addr(dev_err))
+    return k_out, v_out
 
 
 def fused_add_rmsnorm(x, residual, weight, eps, out=None, stream=None):

@@ -15,6 +15,8 @@ namespace {
 constexpr int kDefaultSms = 148;
 constexpr int kMaxPartitions = 1024;        // the reduce kernel's limit
 constexpr int kMinAutoPartitionTokens = 1024;
+constexpr int kTreeWaves = 3;
+constexpr int kMinTreePartitionTokens = 256;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_dtype(int d) { return d == PKV_CACHE_BF16 || d == PKV_CACHE_FP8_E4M3 || d == PKV_CACHE_FP8_E4M3_TOKEN; }
@@ -494,9 +496,30 @@ int pkv_plan_tree(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                     max_context_len, cache_dtype);
     if (st != PKV_OK) return st;
     if (partition_request < -1) return PKV_ERR_INVALID_ARG;
-    plan->partition_tokens = 0;
-    plan->max_partitions = 1;
+    const long long tile = pkv::tree_tile_tokens();
+    long long pt = 0;  // 0: no split
+    if (partition_request > 0) {
+        pt = ((long long)partition_request + tile - 1) / tile * tile;
+    } else if (partition_request == 0) {
+        // about kTreeWaves CTAs per resident slot, so that sequences of unlike
+        // lengths even out, in partitions of at least kMinTreePartitionTokens
+        const long long units = (long long)num_seqs * num_kv_heads *
+                                pkv::tree_row_tiles(max_q_len, num_q_heads / num_kv_heads);
+        const long long want = (2LL * num_sms() * kTreeWaves + units - 1) / (units > 0 ? units : 1);
+        pt = (max_context_len + want - 1) / want;
+        if (pt < kMinTreePartitionTokens) pt = kMinTreePartitionTokens;
+        pt = (pt + tile - 1) / tile * tile;
+    }
+    const long long most = (long long)tile * kMaxPartitions;  // at least this many tokens a partition
+    if (pt > 0 && max_context_len > most * pt / tile) pt = (max_context_len / kMaxPartitions / tile + 1) * tile;
+    if (pt >= max_context_len) pt = 0;
+    plan->partition_tokens = (int)pt;
+    plan->max_partitions = pt > 0 ? (int)((max_context_len + pt - 1) / pt) : 1;
     plan->workspace_bytes = 0;
+    if (pt > 0) {
+        const size_t rows = (size_t)num_seqs * max_q_len * num_q_heads * plan->max_partitions;
+        plan->workspace_bytes = round_up(rows * head_dim * sizeof(float), 256) + round_up(rows * 2 * sizeof(float), 256);
+    }
     return PKV_OK;
 }
 
@@ -552,7 +575,7 @@ int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_c
     a.part_o = nullptr;
     a.part_ml = nullptr;
     if (plan.workspace_bytes > 0) {
-        const size_t rows = (size_t)total_q * num_q_heads * plan.max_partitions;
+        const size_t rows = (size_t)num_seqs * max_q_len * num_q_heads * plan.max_partitions;
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                               round_up(rows * head_dim * sizeof(float), 256));

@@ -255,6 +255,8 @@ struct TreeArgs {
     int *dev_err;
 };
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream);
+int tree_tile_tokens();  // partitions are whole multiples of it
+int tree_row_tiles(int max_q_len, int group);
 
 bool prefill_supported(int head_dim, int group);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);

@@ -1,4 +1,5 @@
-// tree.cu -- attention of a tree of drafted tokens over the paged cache (sm_100a).
+// tree.cu -- attention of a tree of drafted tokens over the paged cache, on the
+// 5th-generation tensor cores (sm_100a).
 //
 // Sequence s brings c = cu_q_lens[s + 1] - cu_q_lens[s] drafted tokens whose
 // K/V are already the last c of its context_lens[s] cached positions. With
@@ -7,121 +8,981 @@
 //   out[j][h] = sum_t softmax_t(scale * q[j][h] . K_t) V_t
 // over those t; a row that sees nothing is zeros.
 //
-// One warp per (draft, query head), the row's d elements spread over the
-// lanes, one pass over the visible tokens with the running maximum and sum.
-#include "pkv_common.cuh"
-#include "pkv_launch.h"
+// What bounds it: a cached (token, KV head) pair is 4 d bytes (bf16) and costs
+// 4 c G d multiply-adds for the c drafts and G heads that share it, c G per
+// byte, and the machine's ratio is some 230: below about that many rows the
+// cache's bytes bound the call, above it the tensor cores do.
+//
+// Work unit: one CTA per (sequence, KV head, 128 rows, partition of the
+// context); a row is a (draft, head of the group) pair. Two CTAs per SM, so
+// that one's start and end overlap the other's stream. Warp roles:
+//   warps 0-3  softmax, one row per thread;
+//   warp 4     producer: copies 64-token K and V tiles into two rings, its lanes
+//              issuing one copy each (blocks smaller than the tile);
+//   warp 5     tensor-memory allocation and the MMA issue, S(0), then
+//              S(j + 1), P V(j), so that the tensor core forms the next scores
+//              while the softmax of tile j runs;
+//   warps 6-7  E4M3 only: widen the V codes of a tile into the ring P V reads.
+// Tensor memory (256 columns): two S buffers of 64 columns and O. P (16-bit
+// pairs) is written over the S it came from and is the A operand of P V.
+//
+// Few rows: with at most 32 (64) rows the tile holds 4 (2) copies of them, and
+// the warps of copy k handle only the k-th quarter (half) of the tile's keys,
+// with weights of zero for the others: a copy is a split of the keys inside
+// the CTA, joined at the end like partitions. A thread then forms 16 (32)
+// exponentials per tile instead of 64.
+//
+// Operands: a bf16 cache feeds bf16 MMAs. E4M3 keys are the operand as they
+// are: Q, scaled per row by a power of two so that its largest element lies in
+// [2^7, 2^8), is the sum of two E4M3 values hi + lo (a bf16 value has 8
+// significant bits, an E4M3 value 4, so the pair is exact down to 2^-9 of the
+// row's largest element and off by at most 2^-17 of it below), and S = hi K^T +
+// lo K^T in binary32 -- the tensor time of one 16-bit product, and no key is
+// converted. V is widened to f16 (exact) with a scale per KV head, where P is
+// rounded to f16, and to bf16(code * scale) with a scale per token, where P is
+// rounded to bf16 (V's range is then the scales'). The softmax runs in base 2
+// with a reference maximum that moves only when a tile exceeds it by 8, and the
+// normaliser sums the rounded weights.
+//
+// Masked keys: a score that the row does not see becomes -inf whatever it
+// was, so its weight is zero; and V elements of drafts that are not finite are
+// set to zero in the staged tile (0 * inf would be NaN for the rows that do
+// not see the draft) and added to exactly the rows that see them at the end.
+//
+// Every wait is bounded (PKV_DEVERR_TIMEOUT); every block id and length is
+// checked before anything is copied (PKV_DEVERR_BOUNDS).
+#include <atomic>
+
+#include "tc_common.cuh"
 
 namespace pkv {
 
 namespace {
 
+using namespace tc;
+
+constexpr int kRows = 128;  // MMA M
+constexpr int kBN = 64;     // keys per tile
+constexpr int kSoftmaxWarps = 4;
+constexpr int kProducerWarp = 4;
+constexpr int kMmaWarp = 5;
+constexpr int kConvWarps = 2;  // E4M3: warps 6, 7
+constexpr int kNK = 2;         // ring depths (tiles)
+constexpr int kNV = 2;
+constexpr uint32_t kTmemCols = 256;  // S0 | S1 | O
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int MODE>
+constexpr int tree_threads() { return MODE == 0 ? 192 : 192 + 32 * kConvWarps; }
+
 template <int D, int MODE>
-__global__ void __launch_bounds__(128) tree_simple_kernel(TreeArgs a, int rows_per_seq) {
-    constexpr int E = D / 32;  // elements per lane
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int blocks_per_seq = (rows_per_seq + 3) / 4;
-    const int s = blockIdx.x / blocks_per_seq;
-    const int item = (blockIdx.x % blocks_per_seq) * 4 + warp;  // draft * num_q_heads + head
-    const int nq = a.num_q_heads;
-    const int j = item / nq, h = item % nq;
-    const int q0 = a.cu_q_lens[s], q1 = a.cu_q_lens[s + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.total_q) {
-        if (threadIdx.x == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
-        return;
-    }
-    const int c = q1 - q0;
-    if (item >= rows_per_seq || j >= c) return;
-    const int ctx = a.context_lens[s];
-    const int kh = h / (nq / a.num_kv_heads);
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((long long)(q0 + j) * nq + h) * D + lane * E;
-    const int32_t *table = a.block_tables + (long long)s * a.max_blocks_per_seq;
-    bool bad = c > a.max_q_len || ctx < c || ctx > a.max_context_len;
-    const int nblk = bad ? 0 : (ctx + a.block_size - 1) / a.block_size;
-    for (int i = lane; i < nblk; i += 32) {
-        const int b = table[i];
-        bad |= b < 0 || b >= a.num_blocks;
-    }
-    float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    if (__any_sync(0xffffffffu, bad)) {
-        if (lane == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
-        for (long long r = j + a.max_q_len; r < c; r += a.max_q_len)  // a chunk longer than the grid expects
-            for (int e = 0; e < E; ++e) out[(r - j) * nq * D + e] = __float2bfloat16_rn(0.f);
-    } else {
-        const int base = ctx - c;
-        const uint32_t *mask = a.mask + (long long)(q0 + j) * a.mask_words;
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + ((long long)(q0 + j) * nq + h) * D + lane * E;
-        float qv[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(q[e]) * a.scale * 1.4426950408889634f;
-        for (int t = 0; t < ctx; ++t) {
-            if (t >= base) {
-                const int u = t - base;
-                if (!((mask[u >> 5] >> (u & 31)) & 1u)) continue;
-            }
-            const long long row = ((long long)table[t / a.block_size] * a.num_kv_heads + kh) * a.block_size +
-                                  t % a.block_size;
-            float kx[E], vx[E];
-            if constexpr (MODE == 0) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    kx[e] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.k_cache)[row * D + lane * E + e]);
-                    vx[e] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.v_cache)[row * D + lane * E + e]);
-                }
-            } else {
-                const float ks = a.k_scale[MODE == 2 ? row : kh], vs = a.v_scale[MODE == 2 ? row : kh];
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 k2 = e4m3x2_to_float2(
-                        *reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(a.k_cache) + row * D + lane * E + e));
-                    const float2 v2 = e4m3x2_to_float2(
-                        *reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(a.v_cache) + row * D + lane * E + e));
-                    kx[e] = k2.x * ks;
-                    kx[e + 1] = k2.y * ks;
-                    vx[e] = v2.x * vs;
-                    vx[e + 1] = v2.y * vs;
-                }
-            }
-            float x = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) x = fmaf(qv[e], kx[e], x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            const float mn = fmaxf(m, x);
-            const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
-            const float p = mn == -INFINITY ? 0.f : exp2f(x - mn);
-            l = l * alpha + p;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(p, vx[e], acc[e] * alpha);
-            m = mn;
-        }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = __float2bfloat16_rn(acc[e] * inv);
+struct TreeLayout {
+    static constexpr bool kFp8 = MODE != 0;
+    static constexpr uint32_t kQ = 0;  // bf16 [D / 64][rows][128 B]; E4M3 hi, lo [rows][D B]
+    static constexpr uint32_t kQBytes = kRows * D * 2;
+    static constexpr uint32_t kKSlot = kBN * D * (kFp8 ? 1 : 2);
+    static constexpr uint32_t kVSlot = kBN * D * 2;   // what P V reads
+    static constexpr uint32_t kRawSlot = kFp8 ? kBN * D : 0;  // E4M3 V codes
+    static constexpr uint32_t kK = kQ + kQBytes;
+    static constexpr uint32_t kV = kK + kNK * kKSlot;
+    static constexpr uint32_t kRaw = kV + kNV * kVSlot;
+    static constexpr uint32_t kKs = kRaw + kNV * kRawSlot;  // per-token scales [slot][kBN] fp32
+    static constexpr uint32_t kVs = kKs + (MODE == 2 ? kNK * kBN * 4 : 0);
+    static constexpr uint32_t kBar = kVs + (MODE == 2 ? kNV * kBN * 4 : 0);
+    static constexpr uint32_t kMl = kBar + 256;  // [2][kRows] fp32: maxima and sums of the copies
+    static constexpr uint32_t kBytes = kMl + 2 * kRows * 4;
+    static constexpr uint32_t kMin = 80u * 1024u;  // at most two CTAs per SM (tensor memory has room for two)
+    static constexpr uint32_t kAlloc = (kBytes + 1024 > kMin ? kBytes + 1024 : kMin);  // + base alignment
+    // the joining of copies goes through [kRows][D + 4] floats over Q and the rings
+    static_assert(kRows * (D + 4) * 4 <= kBar, "copies fit");
+};
+
+struct TreeBars {
+    uint64_t q_full;
+    uint64_t k_full[kNK], k_empty[kNK];
+    uint64_t v_full[kNV], v_empty[kNV];      // the tile P V reads
+    uint64_t raw_full[kNV], raw_empty[kNV];  // E4M3 V codes
+    uint64_t s_full[2];
+    uint64_t p_full[2];
+    uint64_t pv_done;
+    uint64_t drained;
+    uint32_t tmem;
+    int nonfinite;  // a draft's V held an infinity or NaN
+};
+static_assert(sizeof(TreeBars) <= 256, "barrier space");
+
+// 16-byte chunk c of row r in an operand of `D`-byte rows (E4M3): the 128-byte
+// swizzle (D 128) or the 64-byte one (D 64: chunk c of row r at c ^ (r / 2 % 4)).
+template <int D>
+__device__ __forceinline__ uint32_t swz8(int r, int c) {
+    if constexpr (D == 128) return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+    else return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+// Descriptor of a K-major E4M3 operand with D-byte rows.
 template <int D>
-cudaError_t launch_simple(const TreeArgs &a, cudaStream_t stream) {
-    const int rows = a.max_q_len * a.num_q_heads;
-    const long long blocks = (long long)a.num_seqs * ((rows + 3) / 4);
+__device__ __forceinline__ uint64_t desc8(uint32_t saddr) {
+    if constexpr (D == 128) return sw128_desc(saddr, 16, 1024);
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(512 >> 4) << 32) |
+           (1ull << 46) | (4ull << 61);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// N consecutive columns of this thread's tensor-memory lane (N 16, 32 or 64).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, float (&v)[N]) {
+    if constexpr (N == 16) tmem_ld16(taddr, v);
+    else if constexpr (N == 32) tmem_ld32(taddr, v);
+    else tmem_ld64(taddr, v);
+}
+
+// 8 columns into this thread's lane, not waited for.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&w)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// What a CTA works on; the same in every thread.
+struct Unit {
+    int s, kh, q0, c, ctx, base;
+    int row0;    // first row (draft * G + head) of the tile
+    int rows;    // live rows of the tile
+    int per_copy, copies;
+    int t0, t1;  // keys of the partition
+    int tiles;
+    int part, parts;  // partition and number of partitions of this sequence
+};
+
+// Bits [start, start + 32) of a row's view of the context, position start being
+// bit 0: everything below base, the mask's drafts, nothing at or past the end.
+__device__ __forceinline__ uint32_t visible32(const uint32_t *mask, int c, int start, int base) {
+    auto word = [&](int i) -> uint32_t {
+        const int left = c - 32 * i;
+        if (left <= 0) return 0u;
+        const uint32_t w = __ldg(mask + i);
+        return left >= 32 ? w : w & ((1u << left) - 1u);
+    };
+    const int u = start - base;
+    if (u <= -32) return 0xffffffffu;
+    if (u < 0) return ((1u << -u) - 1u) | (word(0) << -u);
+    const int sh = u & 31;
+    const uint32_t lo = word(u >> 5);
+    return sh == 0 ? lo : __funnelshift_r(lo, word((u >> 5) + 1), sh);
+}
+
+// V rows of the staged tile: rows at or past the end become zeros (zero_tail)
+// and elements that are not finite in the drafts' rows too; returns whether
+// there were any. F16: f16 elements, else bf16.
+template <int D, bool F16>
+__device__ __forceinline__ bool mend_v(uint32_t sv, int first, int end, bool zero_tail, int thread, int threads) {
+    constexpr int kChunks = D / 8;
+    constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;
+    bool found = false;
+    const int last = zero_tail ? kBN : end;
+    for (int i = first * kChunks + thread; i < last * kChunks; i += threads) {
+        const int r = i / kChunks, c16 = i % kChunks;
+        const uint32_t at = sv + swz(kBN, r, c16);
+        if (r >= end) {
+            st_shared16(at, make_uint4(0, 0, 0, 0));
+            continue;
+        }
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at));
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if ((w[k] & kExp) == kExp) {
+                w[k] &= 0xFFFF0000u;
+                any = true;
+            }
+            if ((w[k] & (kExp << 16)) == (kExp << 16)) {
+                w[k] &= 0x0000FFFFu;
+                any = true;
+            }
+        }
+        if (any) {
+            st_shared16(at, make_uint4(w[0], w[1], w[2], w[3]));
+            found = true;
+        }
+    }
+    return found;
+}
+
+// Softmax of this warp's rows over the partition: COLS keys of every tile (64
+// / copies). Leaves the reference maximum and the sum of the row (copy).
+template <int D, int MODE, int COLS>
+__device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, TreeBars *bars, uint8_t *sm,
+                                              uint32_t base, uint32_t tmem, float sl2, bool live, int draft,
+                                              int live_warps, float &m_out, float &l_out) {
+    using L = TreeLayout<D, MODE>;
+    constexpr bool kF16 = MODE == 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const int copy = COLS == 64 ? 0 : (warp * 32) / u.per_copy;
+    const int col0 = copy * COLS;
+    const uint32_t *mask = a.mask + static_cast<long long>(u.q0 + draft) * a.mask_words;
+    float m = -INFINITY, l = 0.0f;
+    for (int j = 0; j < u.tiles; ++j) {
+        const int kv0 = u.t0 + j * kBN;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[j & 1], (j >> 1) & 1))) return false;
+        tc_fence_after();
+        const uint32_t ts = tmem + (j & 1) * kBN + lane_base;
+        float x[COLS];
+        tmem_ldn<COLS>(ts + col0, x);
+        if constexpr (MODE == 2) {
+            const int slot = j % kNK;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_full[slot], (j / kNK) & 1))) return false;
+            const float4 *ks = reinterpret_cast<const float4 *>(sm + L::kKs + slot * kBN * 4 + col0 * 4);
+#pragma unroll
+            for (int i = 0; i < COLS / 4; ++i) {
+                const float4 k4 = ks[i];
+                x[4 * i] *= k4.x * sl2;
+                x[4 * i + 1] *= k4.y * sl2;
+                x[4 * i + 2] *= k4.z * sl2;
+                x[4 * i + 3] *= k4.w * sl2;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->k_empty[slot]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < COLS; ++i) x[i] *= sl2;
+        }
+        const bool special = kv0 + kBN > u.base;  // holds drafts, or keys past the end
+        if (special) {
+#pragma unroll
+            for (int h = 0; h < (COLS + 31) / 32; ++h) {
+                const uint32_t vis = live ? visible32(mask, u.c, kv0 + col0 + 32 * h, u.base) : 0u;
+#pragma unroll
+                for (int i = 0; i < (COLS < 32 ? COLS : 32); ++i)
+                    if (!((vis >> i) & 1u)) x[32 * h + i] = -INFINITY;
+            }
+        }
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m8[k] = x[k];
+#pragma unroll
+        for (int i = 8; i < COLS; ++i) m8[i & 7] = fmaxf(m8[i & 7], x[i]);
+        const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+        float alpha = 1.0f;
+        bool rescale = false;
+        if (j == 0) {
+            m = mx;
+        } else {
+            const bool grow = mx > m + 8.0f;
+            rescale = __any_sync(0xffffffffu, grow);
+            if (grow) {
+                alpha = fast_exp2(m - mx);
+                m = mx;
+                l *= alpha;
+            }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;  // nothing seen yet: weights exp2(-inf) = 0
+        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int g = 0; g < COLS / 16; ++g) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p0 = fast_exp2(x[16 * g + 2 * i] - ref), p1 = fast_exp2(x[16 * g + 2 * i + 1] - ref);
+                if constexpr (kF16) {
+                    w[i] = pack_f16(p0, p1);
+                    l4[i & 3] = fma_f16x2_acc(w[i], 0x3C003C00u, l4[i & 3]);
+                } else {
+                    w[i] = pack_bf16(p0, p1);
+                    l4[i & 3] = fma_bf16x2_acc(w[i], 0x3F803F80u, l4[i & 3]);
+                }
+            }
+            tmem_st8(ts + col0 / 2 + 8 * g, w);
+        }
+        if constexpr (COLS < 64) {  // the other copies' keys
+            const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int g = COLS / 16; g < 4; ++g) tmem_st8(ts + ((col0 / 2 + 8 * g) & 31), zero);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        if (rescale) {  // S(j) done implies P V(j - 2) done: the next phase is P V(j - 1)
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (j - 1) & 1))) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+                float v[32];
+                tmem_ld32(tmem + 128 + lane_base + ch * 32, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= alpha;
+                tmem_st32_async(tmem + 128 + lane_base + ch * 32, v);
+            }
+        }
+        if (special) {
+            const int slot = j % kNV;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[slot], (j / kNV) & 1))) return false;
+            const int first = max(0, u.base - kv0), end = min(kBN, u.ctx - kv0);
+            if (mend_v<D, kF16>(base + L::kV + slot * L::kVSlot, first, end, MODE == 0, threadIdx.x, 32 * live_warps))
+                bars->nonfinite = 1;
+            fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[j & 1]);
+    }
+    // S(n - 1) done implies P V(n - 3) done, so the last two phases are waited for
+    // in turn: the parity of the last alone is also that of the third last
+    if (u.tiles > 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (u.tiles - 2) & 1))) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (u.tiles - 1) & 1))) return false;
+    tc_fence_after();
+    m_out = m;
+    l_out = l;
+    return true;
+}
+
+// The elements of the seen drafts' V that are not finite, added to N columns
+// from col of a row of the result (they were zero in the staged tiles).
+template <int D, int MODE, int N>
+__device__ __noinline__ void nonfinite_sum(const TreeArgs &a, const Unit &u, int draft, int col, float *v) {
+    const uint32_t *mask = a.mask + static_cast<long long>(u.q0 + draft) * a.mask_words;
+    const int32_t *table = a.block_tables + static_cast<long long>(u.s) * a.max_blocks_per_seq;
+    for (int t = max(u.t0, u.base); t < u.t1; ++t) {
+        const int d = t - u.base;
+        if (!((__ldg(mask + (d >> 5)) >> (d & 31)) & 1u)) continue;
+        const long long row = (static_cast<long long>(table[t / a.block_size]) * a.num_kv_heads + u.kh) * a.block_size +
+                              t % a.block_size;
+        for (int i = 0; i < N; ++i) {
+            const long long e = row * D + col + i;
+            float x;
+            if constexpr (MODE == 0) {
+                x = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.v_cache)[e]);
+            } else {
+                x = e4m3x2_to_float2(static_cast<const uint8_t *>(a.v_cache)[e]).x;
+                if constexpr (MODE == 2) x = __bfloat162float(__float2bfloat16_rn(x * __ldg(a.v_scale + row)));
+            }
+            if (!isfinite(x)) v[i] += x;
+        }
+    }
+}
+
+template <int D, int MODE, int N>
+__device__ __forceinline__ void add_nonfinite(const TreeArgs &a, const Unit &u, int draft, int col, float (&v)[N]) {
+    float t[N];  // addressed only here, so that v stays in registers
+#pragma unroll
+    for (int i = 0; i < N; ++i) t[i] = v[i];
+    nonfinite_sum<D, MODE, N>(a, u, draft, col, t);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = t[i];
+}
+
+// N result elements from column col of a row: bf16 output, or a partition's
+// binary32 partial.
+template <int D, int N>
+__device__ __forceinline__ void put(const TreeArgs &a, const Unit &u, int draft, int head, int col, const float *v) {
+    const long long nq = a.num_q_heads;
+    if (u.parts == 1) {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + ((u.q0 + draft) * nq + head) * D + col;
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            *reinterpret_cast<uint4 *>(dst + i) =
+                make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
+                           pack_bf16(v[i + 6], v[i + 7]));
+    } else {
+        const long long prow = (static_cast<long long>(u.s) * a.max_q_len + draft) * nq + head;
+        float *dst = a.part_o + (prow * a.num_partitions + u.part) * D + col;
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
+
+__device__ __forceinline__ void put_ml(const TreeArgs &a, const Unit &u, int draft, int head, float m, float l) {
+    if (u.parts == 1) return;
+    const long long prow = (static_cast<long long>(u.s) * a.max_q_len + draft) * a.num_q_heads + head;
+    *reinterpret_cast<float2 *>(a.part_ml + (prow * a.num_partitions + u.part) * 2) = make_float2(m, l);
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(tree_threads<MODE>(), 2)
+    tree_kernel(const __grid_constant__ TreeArgs a, int log2_bs, int log2_g, int row_tiles,
+                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    using L = TreeLayout<D, MODE>;
+    constexpr bool kFp8 = MODE != 0;
+    constexpr int kThreads = tree_threads<MODE>();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *sm = smem_raw + (base - raw);
+    TreeBars *bars = reinterpret_cast<TreeBars *>(sm + L::kBar);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = 1 << log2_g, bs = a.block_size;
+
+    // ------------------------------------------------ the unit, checked
+    Unit u;
+    int b = blockIdx.x;
+    const int rt = b % row_tiles;
+    b /= row_tiles;
+    u.kh = b % a.num_kv_heads;
+    b /= a.num_kv_heads;
+    u.s = b % a.num_seqs;
+    u.part = b / a.num_seqs;
+    u.q0 = __ldg(a.cu_q_lens + u.s);
+    const int q1 = __ldg(a.cu_q_lens + u.s + 1);
+    u.ctx = __ldg(a.context_lens + u.s);
+    if (u.q0 < 0 || q1 < u.q0 || q1 > a.total_q) {
+        if (tid == 0 && rt == 0 && u.kh == 0 && u.part == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
+        return;  // no row of this sequence can be located safely
+    }
+    u.c = q1 - u.q0;
+    u.row0 = rt * kRows;
+    if (u.row0 >= u.c << log2_g) return;
+    if (u.c > a.max_q_len || u.ctx < u.c || u.ctx > a.max_context_len) {
+        if (u.part == 0) {  // zeros for this KV head's rows, whatever the chunk's length
+            const long long n = static_cast<long long>(u.c) << log2_g;
+            for (long long i = rt * kThreads + tid; i < n * (D / 8); i += static_cast<long long>(row_tiles) * kThreads) {
+                const long long r = i / (D / 8);
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                                     ((u.q0 + (r >> log2_g)) * a.num_q_heads + u.kh * G + (r & (G - 1))) * D;
+                *reinterpret_cast<uint4 *>(dst + (i % (D / 8)) * 8) = make_uint4(0, 0, 0, 0);
+            }
+            if (tid == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
+        }
+        return;
+    }
+    u.base = u.ctx - u.c;
+    u.parts = a.partition_tokens > 0 ? (u.ctx + a.partition_tokens - 1) / a.partition_tokens : 1;
+    if (u.part >= u.parts) return;
+    u.t0 = u.part * a.partition_tokens;
+    u.t1 = u.parts > 1 ? min(u.ctx, u.t0 + a.partition_tokens) : u.ctx;
+    u.tiles = (u.t1 - u.t0 + kBN - 1) / kBN;
+    u.rows = min(kRows, (u.c << log2_g) - u.row0);
+    u.per_copy = u.rows <= 32 ? 32 : u.rows <= 64 ? 64 : 128;
+    u.copies = kRows / u.per_copy;
+    const int live_warps = u.copies > 1 ? 4 : (u.rows + 31) / 32;
+    const int32_t *table = a.block_tables + static_cast<long long>(u.s) * a.max_blocks_per_seq;
+    bool bad = false;
+    for (int i = (u.t0 >> log2_bs) + tid; i <= (u.t1 - 1) >> log2_bs; i += kThreads) {
+        const int id = __ldg(table + i);
+        bad |= id < 0 || id >= a.num_blocks;
+    }
+
+    // ------------------------------------------------ setup
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&bars->tmem), kTmemCols);
+    if (tid == 0) {
+        mbar_init(&bars->q_full, kSoftmaxWarps * 32);
+        for (int i = 0; i < kNK; ++i) {
+            mbar_init(&bars->k_full[i], 1);
+            mbar_init(&bars->k_empty[i], MODE == 2 ? 1 + live_warps : 1);  // the scales are read by the softmax
+        }
+        for (int i = 0; i < kNV; ++i) {
+            mbar_init(&bars->v_full[i], kFp8 ? kConvWarps : 1);
+            mbar_init(&bars->v_empty[i], 1);
+            mbar_init(&bars->raw_full[i], 1);
+            mbar_init(&bars->raw_empty[i], kConvWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_full[i], live_warps);
+        }
+        mbar_init(&bars->pv_done, 1);
+        mbar_init(&bars->drained, 1);
+        bars->nonfinite = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    bad = __syncthreads_or(bad);
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+
+    // this softmax thread's row: tile position warp * 32 + lane, copy position / per_copy
+    const int pos = tid & (kRows - 1);
+    const int r = pos & (u.per_copy - 1);
+    const bool live = r < u.rows;
+    const int row = u.row0 + (live ? r : 0);
+    const int draft = row >> log2_g, head = u.kh * G + (row & (G - 1));
+
+    if (bad) {  // zeros, or partials that the join turns into zeros
+        if (warp < kSoftmaxWarps && live && pos < u.per_copy) {
+            const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int i = 0; i < D; i += 8) put<D, 8>(a, u, draft, head, i, zero);
+            put_ml(a, u, draft, head, -INFINITY, -1.0f);
+        }
+        if (tid == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
+    } else if (warp < kSoftmaxWarps) {
+        // ================================================ softmax
+        float sl2 = a.scale * kLog2e;
+        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q);
+        const uint4 *qrow = reinterpret_cast<const uint4 *>(
+            qp + (static_cast<long long>(u.q0 + draft) * a.num_q_heads + head) * D);
+        constexpr int kChunks = D / 8;
+        if constexpr (!kFp8) {
+            for (int i = tid; i < kRows * kChunks; i += kRows) {
+                const int p = i / kChunks, c16 = i % kChunks;
+                const int pr = p & (u.per_copy - 1);
+                const bool ok = pr < u.rows;
+                const int rr = u.row0 + (ok ? pr : 0);
+                const long long e = (static_cast<long long>(u.q0 + (rr >> log2_g)) * a.num_q_heads + u.kh * G +
+                                     (rr & (G - 1))) * D + c16 * 8;
+                cp_async16(base + L::kQ + swz(kRows, p, c16), qp + e, ok ? 16u : 0u);
+            }
+            cp_async_commit();
+            cp_async_wait0();
+        } else {
+            uint4 qv[kChunks];
+            float amax = 0.0f;
+#pragma unroll
+            for (int c16 = 0; c16 < kChunks; ++c16) {
+                qv[c16] = live ? __ldg(qrow + c16) : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {qv[c16].x, qv[c16].y, qv[c16].z, qv[c16].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
+            }
+            // amax < 2^e; times 2^kq it lies in [2^7, 2^8). kq is capped at 60
+            // so that 2^-kq times the softmax scale stays normal: rows that
+            // small have scores of zero to binary32 against any finite key.
+            const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 126;
+            const int kq = min(60, 8 - e);
+            const float qs = __int_as_float((kq + 127) << 23);
+            sl2 *= __int_as_float((127 - kq) << 23);
+            if (MODE == 1) sl2 *= __ldg(a.k_scale + u.kh);
+            if (!(amax <= 3.4e38f)) sl2 = __int_as_float(0x7FC00000);  // an infinite query: E4M3 has none
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {  // 16 elements: one chunk of hi and of lo
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 v4 = qv[2 * c + k / 4];
+                    const uint32_t wv[4] = {v4.x, v4.y, v4.z, v4.w};
+                    const uint32_t w = wv[k & 3];
+                    const float x = bf16lo(w) * qs, y = bf16hi(w) * qs;
+                    const uint16_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+                    const float2 hf = e4m3x2_to_float2(h);
+                    const uint16_t o =
+                        __nv_cvt_float2_to_fp8x2(make_float2(x - hf.x, y - hf.y), __NV_SATFINITE, __NV_E4M3);
+                    if (k & 1) {
+                        hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
+                        lo[k >> 1] |= static_cast<uint32_t>(o) << 16;
+                    } else {
+                        hi[k >> 1] = h;
+                        lo[k >> 1] = o;
+                    }
+                }
+                const uint32_t at = base + L::kQ + swz8<D>(pos, c);
+                st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                st_shared16(at + kRows * D, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q_full);
+
+        bool ok = true;
+        float m = -INFINITY, l = 0.0f;
+        if (warp < live_warps) {
+            if (u.copies == 4)
+                ok = softmax_tiles<D, MODE, 16>(a, u, bars, sm, base, tmem, sl2, live, draft, live_warps, m, l);
+            else if (u.copies == 2)
+                ok = softmax_tiles<D, MODE, 32>(a, u, bars, sm, base, tmem, sl2, live, draft, live_warps, m, l);
+            else
+                ok = softmax_tiles<D, MODE, 64>(a, u, bars, sm, base, tmem, sl2, live, draft, live_warps, m, l);
+        }
+        if (!ok && lane == 0) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
+        const float vsc = MODE == 1 ? __ldg(a.v_scale + u.kh) : 1.0f;
+        const uint32_t tmem_o = tmem + 128 + (static_cast<uint32_t>(warp * 32) << 16);
+        named_sync(1, kSoftmaxWarps * 32);  // (also: nonfinite is complete)
+        const bool nonfinite = bars->nonfinite != 0;
+        if (u.copies == 1) {
+            if (warp < live_warps && ok) {
+                const float inv = l == 0.0f ? 0.0f : vsc / l;
+#pragma unroll
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    float v[32];
+                    tmem_ld32(tmem_o + ch * 32, v);
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = l == 0.0f ? 0.0f : v[i] * inv;
+                        if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, ch * 32, v);
+                        put<D, 32>(a, u, draft, head, ch * 32, v);
+                    }
+                }
+                if (live) put_ml(a, u, draft, head, m, l);
+            }
+        } else {
+            // join the copies: their sums to one maximum, their O through shared memory
+            float *ml = reinterpret_cast<float *>(sm + L::kMl);
+            float *o = reinterpret_cast<float *>(sm);  // [kRows][D + 4], over Q and the rings
+            ml[pos] = m;
+            ml[kRows + pos] = l;
+            named_sync(1, kSoftmaxWarps * 32);
+            float top = -INFINITY, sum = 0.0f;
+            for (int k = 0; k < u.copies; ++k) top = fmaxf(top, ml[k * u.per_copy + r]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            for (int k = 0; k < u.copies; ++k)
+                sum = fmaf(fast_exp2(ml[k * u.per_copy + r] - ref), ml[kRows + k * u.per_copy + r], sum);
+            const float w = m == -INFINITY ? 0.0f : fast_exp2(m - ref);
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+                float v[32];
+                tmem_ld32(tmem_o + ch * 32, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4 *>(o + pos * (D + 4) + ch * 32 + i) =
+                        l == 0.0f ? make_float4(0, 0, 0, 0)
+                                  : make_float4(v[i] * w, v[i + 1] * w, v[i + 2] * w, v[i + 3] * w);
+            }
+            named_sync(1, kSoftmaxWarps * 32);
+            if (live && ok) {
+                // this thread: D / copies columns of its row
+                const float inv = sum == 0.0f ? 0.0f : vsc / sum;
+                const int width = D / u.copies, first = (pos / u.per_copy) * width;
+                for (int c8 = 0; c8 < width; c8 += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        float4 acc = *reinterpret_cast<const float4 *>(o + r * (D + 4) + first + c8 + i);
+                        for (int k = 1; k < u.copies; ++k) {
+                            const float4 x =
+                                *reinterpret_cast<const float4 *>(o + (k * u.per_copy + r) * (D + 4) + first + c8 + i);
+                            acc.x += x.x;
+                            acc.y += x.y;
+                            acc.z += x.z;
+                            acc.w += x.w;
+                        }
+                        v[i] = acc.x * inv;
+                        v[i + 1] = acc.y * inv;
+                        v[i + 2] = acc.z * inv;
+                        v[i + 3] = acc.w * inv;
+                    }
+                    if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, first + c8, v);
+                    put<D, 8>(a, u, draft, head, first + c8, v);
+                }
+                if (pos < u.per_copy) put_ml(a, u, draft, head, top, sum);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kProducerWarp) {
+        // ================================================ producer
+        constexpr int kHalves = D / 64;
+        int issued_k = 0, issued_v = 0;
+        // block ids, 32 at a time, the next 32 already loading
+        const int first_blk = u.t0 >> log2_bs, last_blk = (u.t1 - 1) >> log2_bs;
+        int win = first_blk;
+        int id = __ldg(table + min(win + lane, last_blk)), id_next = __ldg(table + min(win + 32 + lane, last_blk));
+        bool ok = true;
+        for (int j = 0; j < u.tiles; ++j) {
+            const int kv0 = u.t0 + j * kBN;
+            const int blk0 = kv0 >> log2_bs;
+            if (blk0 >= win + 32) {
+                win += 32;
+                id = id_next;
+                id_next = __ldg(table + min(win + 32 + lane, last_blk));
+            }
+            const int run = min(bs, kBN);  // rows per copy
+            const int n = bs >= kBN ? 1 : (min(kv0 + kBN, u.t1) - kv0 + bs - 1) >> log2_bs;
+            // lane i handles block i of the tile (bf16: lane 2 i + half)
+            const int bi = kFp8 ? lane : lane / kHalves;
+            const int half = kFp8 ? 0 : lane % kHalves;
+            const int blk = __shfl_sync(0xffffffffu, id, (blk0 - win + min(bi, n - 1)) & 31);
+            const long long prow = (static_cast<long long>(blk) * a.num_kv_heads + u.kh) * bs + (kv0 & (bs - 1));
+            const bool mine = bi < n;
+            auto stage = [&](bool is_k) -> bool {
+                const int slot = is_k ? j % kNK : j % kNV, use = is_k ? j / kNK : j / kNV;
+                uint64_t *empty = is_k ? &bars->k_empty[slot] : kFp8 ? &bars->raw_empty[slot] : &bars->v_empty[slot];
+                uint64_t *full = is_k ? &bars->k_full[slot] : kFp8 ? &bars->raw_full[slot] : &bars->v_full[slot];
+                if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (use - 1) & 1))) return false;
+                const uint32_t bytes = static_cast<uint32_t>(n * run) * (D * (kFp8 ? 1 : 2) + (MODE == 2 ? 4 : 0));
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                if (mine) {
+                    if constexpr (!kFp8) {
+                        const uint32_t dst = base + (is_k ? L::kK + slot * L::kKSlot : L::kV + slot * L::kVSlot);
+                        tma_load_2d(dst + half * kBN * 128 + bi * run * 128, is_k ? &map_k : &map_v, half * 64,
+                                    static_cast<int>(prow), full);
+                    } else {
+                        if (is_k)
+                            tma_load_2d(base + L::kK + slot * L::kKSlot + bi * run * D, &map_k, 0,
+                                        static_cast<int>(prow), full);
+                        else
+                            bulk_g2s(sm + L::kRaw + slot * L::kRawSlot + bi * run * D,
+                                     static_cast<const uint8_t *>(a.v_cache) + prow * D, run * D, full);
+                        if constexpr (MODE == 2)
+                            bulk_g2s(sm + (is_k ? L::kKs : L::kVs) + slot * kBN * 4 + bi * run * 4,
+                                     (is_k ? a.k_scale : a.v_scale) + prow, run * 4, full);
+                    }
+                }
+                return true;
+            };
+            if (!stage(true)) {
+                ok = false;
+                break;
+            }
+            issued_k = j + 1;
+            if (!stage(false)) {
+                ok = false;
+                break;
+            }
+            issued_v = j + 1;
+        }
+        __syncwarp();
+        if (!ok && lane == 0) {
+            set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
+            // copies still in flight: wait for them before the CTA exits
+            for (int j = max(0, issued_k - kNK); j < issued_k; ++j) mbar_wait(&bars->k_full[j % kNK], (j / kNK) & 1);
+            for (int j = max(0, issued_v - kNV); j < issued_v; ++j)
+                mbar_wait(kFp8 ? &bars->raw_full[j % kNV] : &bars->v_full[j % kNV], (j / kNV) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ================================================ MMA issue
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = kFp8 ? idesc_f16(kRows, kBN, false) : idesc_bf16(kRows, kBN, false);
+            constexpr uint32_t kIdescPV = MODE == 1 ? idesc_f16(kRows, D, true) : idesc_bf16(kRows, D, true);
+            const uint32_t sq = base + L::kQ;
+            auto issue_s = [&](int j) {
+                const uint32_t sk = base + L::kK + (j % kNK) * L::kKSlot;
+                const uint32_t ts = tmem + (j & 1) * kBN;
+                if constexpr (kFp8) {  // E4M3: format code 0 for A and B, 32 elements per step; hi, then lo
+#pragma unroll
+                    for (int kk = 0; kk < 2 * (D / 32); ++kk) {
+                        const uint32_t off = static_cast<uint32_t>((kk % (D / 32)) * 32);
+                        mma_f8(ts, desc8<D>(sq + (kk / (D / 32)) * kRows * D + off), desc8<D>(sk + off), kIdescS,
+                               kk > 0 ? 1u : 0u);
+                    }
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t ao = static_cast<uint32_t>((kk >> 2) * kRows * 128 + (kk & 3) * 32);
+                        const uint32_t bo = static_cast<uint32_t>((kk >> 2) * kBN * 128 + (kk & 3) * 32);
+                        mma_bf16(ts, sw128_desc(sq + ao, 16, 1024), sw128_desc(sk + bo, 16, 1024), kIdescS,
+                                 kk > 0 ? 1u : 0u);
+                    }
+                }
+                mma_commit(&bars->k_empty[j % kNK]);
+                mma_commit(&bars->s_full[j & 1]);
+            };
+            bool ok = mbar_wait(&bars->q_full, 0) && mbar_wait(&bars->k_full[0], 0);
+            tc_fence_after();
+            if (ok) issue_s(0);
+            for (int j = 0; ok && j < u.tiles; ++j) {
+                if (j + 1 < u.tiles) {  // its S buffer was P of tile j - 1, which P V(j - 1) read before
+                    ok = mbar_wait(&bars->k_full[(j + 1) % kNK], ((j + 1) / kNK) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(j + 1);
+                }
+                ok = mbar_wait(&bars->p_full[j & 1], (j >> 1) & 1) && mbar_wait(&bars->v_full[j % kNV], (j / kNV) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sv = base + L::kV + (j % kNV) * L::kVSlot;
+#pragma unroll
+                for (int kk = 0; kk < kBN / 16; ++kk)
+                    mma_bf16_ts(tmem + 128, tmem + (j & 1) * kBN + kk * 8,
+                                sw128_desc(sv + static_cast<uint32_t>(kk * 16 * 128), kBN * 128, 1024), kIdescPV,
+                                (j > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(&bars->v_empty[j % kNV]);
+                mma_commit(&bars->pv_done);
+            }
+            if (!ok) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
+            // every MMA issued so far has finished before tensor memory is freed
+            mma_commit(&bars->drained);
+            mbar_wait(&bars->drained, 0);
+        }
+        __syncwarp();
+    } else if constexpr (kFp8) {
+        // ================================================ V converters (warps 6, 7)
+        constexpr int kCT = kConvWarps * 32;
+        constexpr int kCPR = D / 16;  // 16-code chunks per row
+        const int ct = tid - 192;
+        bool ok = true;
+        for (int j = 0; j < u.tiles; ++j) {
+            const int slot = j % kNV;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->raw_full[slot], (j / kNV) & 1)) ||
+                (j >= kNV && !__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[slot], (j / kNV - 1) & 1)))) {
+                ok = false;
+                break;
+            }
+            const int end = min(kBN, u.t1 - (u.t0 + j * kBN));  // rows past the end become zeros
+            const uint8_t *src = sm + L::kRaw + slot * L::kRawSlot;
+            const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + slot * kBN;
+            const uint32_t dst = base + L::kV + slot * L::kVSlot;
+#pragma unroll
+            for (int i0 = 0; i0 < kBN * kCPR; i0 += kCT) {
+                const int i = i0 + ct;
+                const int rr = i / kCPR, cc = i % kCPR;
+                const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
+                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                if (rr < end) {
+                    if constexpr (MODE == 2) {
+                        const float s = vs[rr];
+                        lo = e4m3x8_scaled_bf16x8(make_uint2(w.x, w.y), s);
+                        hi = e4m3x8_scaled_bf16x8(make_uint2(w.z, w.w), s);
+                    } else {
+                        const uint2 h0 = e4m3x4_to_f16x4(w.x), h1 = e4m3x4_to_f16x4(w.y);
+                        const uint2 h2 = e4m3x4_to_f16x4(w.z), h3 = e4m3x4_to_f16x4(w.w);
+                        lo = make_uint4(h0.x, h0.y, h1.x, h1.y);
+                        hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
+                    }
+                }
+                st_shared16(dst + swz(kBN, rr, 2 * cc), lo);
+                st_shared16(dst + swz(kBN, rr, 2 * cc + 1), hi);
+            }
+            fence_proxy_async_smem();  // P V reads the tile through the async proxy
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars->v_full[slot]);
+                mbar_arrive(&bars->raw_empty[slot]);
+            }
+        }
+        if (!ok && lane == 0) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Join of a sequence's partitions: one warp per (draft, query head).
+constexpr int kJoinWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(TreeArgs a, int blocks_per_seq) {
+    constexpr int E = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = blockIdx.x / blocks_per_seq;
+    const int item = (blockIdx.x % blocks_per_seq) * kJoinWarps + warp;  // draft * num_q_heads + head
+    const int q0 = __ldg(a.cu_q_lens + s), q1 = __ldg(a.cu_q_lens + s + 1), ctx = __ldg(a.context_lens + s);
+    if (q0 < 0 || q1 < q0 || q1 > a.total_q) return;
+    const int c = q1 - q0;
+    if (c > a.max_q_len || ctx < c || ctx > a.max_context_len) return;  // the attention kernel's zeros
+    if (item >= c * a.num_q_heads) return;
+    const int parts = (ctx + a.partition_tokens - 1) / a.partition_tokens;
+    if (parts <= 1) return;
+    const long long prow = static_cast<long long>(s) * a.max_q_len * a.num_q_heads + item;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + prow * a.num_partitions;
+    const float *po = a.part_o + prow * a.num_partitions * D + lane * E;
+    float top = -INFINITY;
+    bool bad = false;
+    for (int i = lane; i < parts; i += 32) {
+        const float2 x = ml[i];
+        top = fmaxf(top, x.x);
+        bad |= x.y < 0.0f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    bad = __any_sync(0xffffffffu, bad);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    float sum = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+        const float2 x = ml[i];
+        if (x.y == 0.0f) continue;
+        const float w = fast_exp2(x.x - ref) * x.y;
+        sum += w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, po[static_cast<long long>(i) * D + e], acc[e]);
+    }
+    const float inv = (bad || sum == 0.0f) ? 0.0f : 1.0f / sum;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (static_cast<long long>(q0) * a.num_q_heads + item) * D +
+                         lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        const uint32_t w = bad ? 0u : pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+        *reinterpret_cast<uint32_t *>(out + e) = w;
+    }
+}
+
+// The pool as a 2-D tensor of rows: boxes of 64 bf16 columns (128-byte swizzle)
+// or whole E4M3 rows (128- or 64-byte swizzle) of min(block_size, kBN) rows.
+bool make_map(CUtensorMap *map, const void *pool, const TreeArgs &a) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const bool fp8 = a.mode != 0;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.head_dim),
+                                static_cast<cuuint64_t>(a.num_blocks) * a.num_kv_heads * a.block_size};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.head_dim) * (fp8 ? 1 : 2)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(fp8 ? a.head_dim : 64),
+                               static_cast<cuuint32_t>(a.block_size < kBN ? a.block_size : kBN)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              fp8 && a.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int MODE>
+cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
+    using L = TreeLayout<D, MODE>;
+    const int g = a.num_q_heads / a.num_kv_heads;
+    int log2_bs = 0, log2_g = 0;
+    while ((1 << log2_bs) < a.block_size) ++log2_bs;
+    while ((1 << log2_g) < g) ++log2_g;
+    // row coordinates of the tensor maps are int32
+    if (a.num_blocks * a.num_kv_heads * a.block_size > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const long long row_tiles = (static_cast<long long>(a.max_q_len) * g + kRows - 1) / kRows;
+    const long long units = row_tiles * a.num_kv_heads * a.num_seqs;
+    if (row_tiles > 0x7fffffffLL || units > 0x7fffffffLL / a.num_partitions) return cudaErrorInvalidConfiguration;
+    CUtensorMap mk, mv;
+    memset(&mv, 0, sizeof(mv));
+    if (!make_map(&mk, a.k_cache, a) || (MODE == 0 && !make_map(&mv, a.v_cache, a))) return cudaErrorInvalidValue;
+    auto kern = tree_kernel<D, MODE>;
+    static std::atomic<unsigned long long> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::kAlloc));
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    kern<<<static_cast<unsigned>(units * a.num_partitions), tree_threads<MODE>(), L::kAlloc, stream>>>(
+        a, log2_bs, log2_g, static_cast<int>(row_tiles), mk, mv);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.partition_tokens == 0) return e;
+    const long long per_seq = (static_cast<long long>(a.max_q_len) * a.num_q_heads + kJoinWarps - 1) / kJoinWarps;
+    const long long blocks = per_seq * a.num_seqs;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (a.mode == 2)
-        tree_simple_kernel<D, 2><<<(unsigned)blocks, 128, 0, stream>>>(a, rows);
-    else if (a.mode == 1)
-        tree_simple_kernel<D, 1><<<(unsigned)blocks, 128, 0, stream>>>(a, rows);
-    else
-        tree_simple_kernel<D, 0><<<(unsigned)blocks, 128, 0, stream>>>(a, rows);
+    tree_join_kernel<D><<<static_cast<unsigned>(blocks), 32 * kJoinWarps, 0, stream>>>(a, static_cast<int>(per_seq));
     return cudaGetLastError();
 }
 
 }  // namespace
 
+int tree_tile_tokens() { return kBN; }
+int tree_row_tiles(int max_q_len, int group) {
+    return static_cast<int>((static_cast<long long>(max_q_len) * group + kRows - 1) / kRows);
+}
+
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
-    return a.head_dim == 128 ? launch_simple<128>(a, stream) : launch_simple<64>(a, stream);
+    if (a.head_dim == 128)
+        return a.mode == 0 ? launch_mode<128, 0>(a, stream)
+                           : a.mode == 1 ? launch_mode<128, 1>(a, stream) : launch_mode<128, 2>(a, stream);
+    return a.mode == 0 ? launch_mode<64, 0>(a, stream)
+                       : a.mode == 1 ? launch_mode<64, 1>(a, stream) : launch_mode<64, 2>(a, stream);
 }
 
 }  // namespace pkv

@@ -104,7 +104,8 @@ struct TreeBars {
     uint64_t raw_full[kNV], raw_empty[kNV];  // E4M3 V codes
     uint64_t s_full[2];
     uint64_t p_full[2];
-    uint64_t pv_done;
+    uint64_t pv_done;  // per tile; S(j) done and P of tile j missing leave it in phase j - 1 or j
+    uint64_t o_done;   // after the last tile
     uint64_t drained;
     uint32_t tmem;
     int nonfinite;  // a draft's V held an infinity or NaN
@@ -349,10 +350,9 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_full[j & 1]);
     }
-    // S(n - 1) done implies P V(n - 3) done, so the last two phases are waited for
-    // in turn: the parity of the last alone is also that of the third last
-    if (u.tiles > 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (u.tiles - 2) & 1))) return false;
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (u.tiles - 1) & 1))) return false;
+    // its own barrier: pv_done may be one or two phases further by now, and a
+    // parity cannot tell which
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_done, 0))) return false;
     tc_fence_after();
     m_out = m;
     l_out = l;
@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
             mbar_init(&bars->p_full[i], live_warps);
         }
         mbar_init(&bars->pv_done, 1);
+        mbar_init(&bars->o_done, 1);
         mbar_init(&bars->drained, 1);
         bars->nonfinite = 0;
         fence_barrier_init();
@@ -799,6 +800,7 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                                 (j > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(&bars->v_empty[j % kNV]);
                 mma_commit(&bars->pv_done);
+                if (j + 1 == u.tiles) mma_commit(&bars->o_done);
             }
             if (!ok) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
             // every MMA issued so far has finished before tensor memory is freed

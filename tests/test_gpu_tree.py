@@ -266,6 +266,20 @@ def test_same_call_gives_the_same_bits_and_graphs_replay():
         close(c, outs[0], ref, mag)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
+def test_many_ragged_trees_again_and_again(cache):
+    """More CTAs than fit at once, rows that leave warps without work, calls
+    back to back: every wait ends and every call gives the same bits."""
+    ql = [1 + (7 * i) % 40 for i in range(48)]
+    c = make(ql, [q + (131 * i) % 900 for i, q in enumerate(ql)], 32, 8, 128, 16, cache, seed=31)
+    want = check(c)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [call(c, dev_err=err) for _ in range(40)]
+    assert K.read_device_error(err) == K.PKV_OK
+    for o in outs:
+        assert torch.equal(o, want)
+
+
 def test_on_another_stream_with_its_own_workspace():
     c = make([8, 30], [3000, 900], 8, 2, 128, 16, "bf16", seed=24)
     want = call(c).clone()

@@ -466,12 +466,17 @@ PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int num_kv_heads, int h
  *  tree_mask      [total_q][mask_words] uint32: bit u % 32 of word u / 32
  *  cu_q_lens      [num_seqs + 1] int32: 0, then running sums of the c_i
  *  context_lens   [num_seqs] int32, c_i <= context_lens[i] <= max_context_len
- *  max_q_len      host-known bound on every c_i, at most 32 * mask_words
+ *  max_q_len      host-known bound on every c_i, at most 32 * mask_words and 65536
  *  max_context_len  host-known bound on every context, at most
  *                 max_blocks_per_seq * block_size
- *  partition_request, workspace  as for pkv_paged_attention_decode, with the
- *                 plan of pkv_plan_tree (256-byte aligned; calls that may
- *                 overlap on the GPU need separate workspaces)
+ *  shares         into how many equal shares the work is cut, one thread block
+ *                 each; 0: two per SM (fewer where the work is small). At most
+ *                 4096. Sequences need not be alike: a share ends where it
+ *                 ends, and partial results of what it cuts are joined
+ *  workspace      device scratch of at least the plan's workspace_bytes,
+ *                 256-byte aligned (may be NULL when that is 0); contents need
+ *                 not be initialised and are clobbered, so calls that may
+ *                 overlap on the GPU need workspaces of their own
  *  out            [total_q][num_q_heads][head_dim] bf16; rows at and beyond
  *                 cu_q_lens[num_seqs] are left as they are
  *
@@ -483,17 +488,21 @@ PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int num_kv_heads, int h
  * max_q_len or than its context, a context above max_context_len, or a block
  * id outside the pool (the sequence's rows are zeros) set PKV_DEVERR_BOUNDS.
  */
+typedef struct {
+    int shares;             /* thread blocks */
+    size_t workspace_bytes; /* 0 with one share */
+} pkv_tree_plan;
+
 PKV_API int pkv_plan_tree(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
-                          int max_q_len, int max_context_len, int cache_dtype, int partition_request,
-                          pkv_decode_plan *plan);
+                          int max_q_len, int max_context_len, int cache_dtype, int shares, pkv_tree_plan *plan);
 PKV_API int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_cache,
                                      const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cu_q_lens,
                                      const int32_t *context_lens, const uint32_t *tree_mask, int mask_words,
                                      int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
                                      int block_size, int64_t num_blocks, float scale, int cache_dtype,
                                      const float *k_scale, const float *v_scale, int max_q_len, int max_context_len,
-                                     int partition_request, void *workspace, size_t workspace_bytes, void *out,
-                                     int *dev_err, void *stream);
+                                     int shares, void *workspace, size_t workspace_bytes, void *out, int *dev_err,
+                                     void *stream);
 
 /*
  * pkv_compact_kvcache: after a tree's verification, the cached rows of the

@@ -15,8 +15,8 @@ namespace {
 constexpr int kDefaultSms = 148;
 constexpr int kMaxPartitions = 1024;        // the reduce kernel's limit
 constexpr int kMinAutoPartitionTokens = 1024;
-constexpr int kTreeWaves = 3;
-constexpr int kMinTreePartitionTokens = 256;
+constexpr int kMaxTreeShares = 4096;
+constexpr int kMaxTreeDrafts = 1 << 16;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_dtype(int d) { return d == PKV_CACHE_BF16 || d == PKV_CACHE_FP8_E4M3 || d == PKV_CACHE_FP8_E4M3_TOKEN; }
@@ -480,6 +480,8 @@ int check_tree_shape(int num_seqs, int num_q_heads, int num_kv_heads, int head_d
                      int max_context_len, int cache_dtype) {
     if (num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || max_q_len < 1 || max_context_len < 1)
         return PKV_ERR_INVALID_ARG;
+    if (max_q_len > kMaxTreeDrafts || max_context_len > INT32_MAX - 1024 || num_kv_heads > 65535)
+        return PKV_ERR_INVALID_ARG;
     if (num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
     if (!valid_dtype(cache_dtype)) return PKV_ERR_INVALID_ARG;
     if (!pow2(block_size) || block_size < 8 || block_size > 1024) return PKV_ERR_INVALID_ARG;
@@ -490,34 +492,16 @@ int check_tree_shape(int num_seqs, int num_q_heads, int num_kv_heads, int head_d
 }  // namespace
 
 int pkv_plan_tree(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_q_len,
-                  int max_context_len, int cache_dtype, int partition_request, pkv_decode_plan *plan) {
+                  int max_context_len, int cache_dtype, int shares, pkv_tree_plan *plan) {
     if (!plan) return PKV_ERR_INVALID_ARG;
     const int st = check_tree_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len,
                                     max_context_len, cache_dtype);
     if (st != PKV_OK) return st;
-    if (partition_request < -1) return PKV_ERR_INVALID_ARG;
-    const long long tile = pkv::tree_tile_tokens();
-    long long pt = 0;  // 0: no split
-    if (partition_request > 0) {
-        pt = ((long long)partition_request + tile - 1) / tile * tile;
-    } else if (partition_request == 0) {
-        // about kTreeWaves CTAs per resident slot, so that sequences of unlike
-        // lengths even out, in partitions of at least kMinTreePartitionTokens
-        const long long units = (long long)num_seqs * num_kv_heads *
-                                pkv::tree_row_tiles(max_q_len, num_q_heads / num_kv_heads);
-        const long long want = (2LL * num_sms() * kTreeWaves + units - 1) / (units > 0 ? units : 1);
-        pt = (max_context_len + want - 1) / want;
-        if (pt < kMinTreePartitionTokens) pt = kMinTreePartitionTokens;
-        pt = (pt + tile - 1) / tile * tile;
-    }
-    const long long most = (long long)tile * kMaxPartitions;  // at least this many tokens a partition
-    if (pt > 0 && max_context_len > most * pt / tile) pt = (max_context_len / kMaxPartitions / tile + 1) * tile;
-    if (pt >= max_context_len) pt = 0;
-    plan->partition_tokens = (int)pt;
-    plan->max_partitions = pt > 0 ? (int)((max_context_len + pt - 1) / pt) : 1;
+    if (shares < 0 || shares > kMaxTreeShares) return PKV_ERR_INVALID_ARG;
+    plan->shares = shares > 0 ? shares : 2 * num_sms();
     plan->workspace_bytes = 0;
-    if (pt > 0) {
-        const size_t rows = (size_t)num_seqs * max_q_len * num_q_heads * plan->max_partitions;
+    if (plan->shares > 1) {
+        const size_t rows = (size_t)2 * plan->shares * pkv::tree_slot_rows(max_q_len, num_q_heads / num_kv_heads);
         plan->workspace_bytes = round_up(rows * head_dim * sizeof(float), 256) + round_up(rows * 2 * sizeof(float), 256);
     }
     return PKV_OK;
@@ -528,11 +512,11 @@ int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_c
                              const uint32_t *tree_mask, int mask_words, int num_seqs, int total_q, int num_q_heads,
                              int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
                              int cache_dtype, const float *k_scale, const float *v_scale, int max_q_len,
-                             int max_context_len, int partition_request, void *workspace, size_t workspace_bytes,
+                             int max_context_len, int shares, void *workspace, size_t workspace_bytes,
                              void *out, int *dev_err, void *stream) {
-    pkv_decode_plan plan;
+    pkv_tree_plan plan;
     const int st = pkv_plan_tree(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len,
-                                 max_context_len, cache_dtype, partition_request, &plan);
+                                 max_context_len, cache_dtype, shares, &plan);
     if (st != PKV_OK) return st;
     if (total_q < 0 || mask_words < 1 || (long long)mask_words * 32 < max_q_len) return PKV_ERR_INVALID_ARG;
     if (!q || !k_cache || !v_cache || !block_tables || !cu_q_lens || !context_lens || !tree_mask || !out)
@@ -570,12 +554,12 @@ int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_c
     a.v_scale = v_scale;
     a.max_q_len = max_q_len;
     a.max_context_len = max_context_len;
-    a.partition_tokens = plan.partition_tokens;
-    a.num_partitions = plan.max_partitions;
+    a.max_shares = plan.shares;
+    a.min_share = shares > 0 ? 1 : pkv::tree_min_share();
     a.part_o = nullptr;
     a.part_ml = nullptr;
     if (plan.workspace_bytes > 0) {
-        const size_t rows = (size_t)num_seqs * max_q_len * num_q_heads * plan.max_partitions;
+        const size_t rows = (size_t)2 * plan.shares * pkv::tree_slot_rows(max_q_len, num_q_heads / num_kv_heads);
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                               round_up(rows * head_dim * sizeof(float), 256));

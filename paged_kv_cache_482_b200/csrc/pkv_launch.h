@@ -247,16 +247,16 @@ struct TreeArgs {
     const float *v_scale;
     int max_q_len;
     int max_context_len;
-    int partition_tokens;  // 0: one partition
-    int num_partitions;
-    float *part_o;
-    float *part_ml;
+    int max_shares;  // CTAs; shares of at least min_share tiles of work
+    int min_share;
+    float *part_o;   // [2 max_shares][tree_slot_rows][head_dim]
+    float *part_ml;  // [2 max_shares][tree_slot_rows][2]
     void *out;
     int *dev_err;
 };
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream);
-int tree_tile_tokens();  // partitions are whole multiples of it
-int tree_row_tiles(int max_q_len, int group);
+int tree_slot_rows(int max_q_len, int group);
+int tree_min_share();
 
 bool prefill_supported(int head_dim, int group);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);

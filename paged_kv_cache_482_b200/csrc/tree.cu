@@ -13,9 +13,13 @@
 // byte, and the machine's ratio is some 230: below about that many rows the
 // cache's bytes bound the call, above it the tensor cores do.
 //
-// Work unit: one CTA per (sequence, KV head, 128 rows, partition of the
-// context); a row is a (draft, head of the group) pair. Two CTAs per SM, so
-// that one's start and end overlap the other's stream. Warp roles:
+// Work: a unit is (sequence, KV head, 128 rows), a row a (draft, head of the
+// group) pair. The units' key tiles, laid end to end, are cut into equal
+// shares, one per CTA, two CTAs per SM (one's joins and starts overlap the
+// other's stream): lengths need not be alike, no CTA idles, and a unit is cut
+// only where a share ends. A CTA computes its share from the lengths; the
+// partial results of cut units (at most two per CTA) go to the workspace and a
+// second kernel joins them. Warp roles:
 //   warps 0-3  softmax, one row per thread;
 //   warp 4     producer: copies 64-token K and V tiles into two rings, its lanes
 //              issuing one copy each (blocks smaller than the tile);
@@ -29,7 +33,7 @@
 // Few rows: with at most 32 (64) rows the tile holds 4 (2) copies of them, and
 // the warps of copy k handle only the k-th quarter (half) of the tile's keys,
 // with weights of zero for the others: a copy is a split of the keys inside
-// the CTA, joined at the end like partitions. A thread then forms 16 (32)
+// the CTA, joined at the end of the unit. A thread then forms 16 (32)
 // exponentials per tile instead of 64.
 //
 // Operands: a bf16 cache feeds bf16 MMAs. E4M3 keys are the operand as they
@@ -90,11 +94,12 @@ struct TreeLayout {
     static constexpr uint32_t kVs = kKs + (MODE == 2 ? kNK * kBN * 4 : 0);
     static constexpr uint32_t kBar = kVs + (MODE == 2 ? kNV * kBN * 4 : 0);
     static constexpr uint32_t kMl = kBar + 256;  // [2][kRows] fp32: maxima and sums of the copies
+    // results leave through [kRows][kOutCols + 4] floats over Q, free by then
+    static constexpr int kOutCols = D / 4;
     static constexpr uint32_t kBytes = kMl + 2 * kRows * 4;
     static constexpr uint32_t kMin = 80u * 1024u;  // at most two CTAs per SM (tensor memory has room for two)
     static constexpr uint32_t kAlloc = (kBytes + 1024 > kMin ? kBytes + 1024 : kMin);  // + base alignment
-    // the joining of copies goes through [kRows][D + 4] floats over Q and the rings
-    static_assert(kRows * (D + 4) * 4 <= kBar, "copies fit");
+    static_assert(kRows * (kOutCols + 4) * 4 <= kQBytes, "results fit");
 };
 
 struct TreeBars {
@@ -105,10 +110,13 @@ struct TreeBars {
     uint64_t s_full[2];
     uint64_t p_full[2];
     uint64_t pv_done;  // per tile; S(j) done and P of tile j missing leave it in phase j - 1 or j
-    uint64_t o_done;   // after the last tile
+    uint64_t o_done;   // per unit, after its last tile
     uint64_t drained;
     uint32_t tmem;
-    int nonfinite;  // a draft's V held an infinity or NaN
+    int nonfinite[2];  // by unit parity: a draft's V held an infinity or NaN
+    int bad[2];        // by unit parity: a block id outside the pool
+    int failed;        // a softmax wait gave up
+    long long scan[9]; // share computation
 };
 static_assert(sizeof(TreeBars) <= 256, "barrier space");
 
@@ -164,15 +172,165 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&w)[8])
                  : "memory");
 }
 
-// What a CTA works on; the same in every thread.
+// Cost of a unit besides its tiles (query loads, first scores, results), in tiles.
+constexpr int kUnitCost = 3;
+// Shares are at least this long where the number of shares is chosen here: a
+// shorter one spends most of its time starting and joining.
+constexpr int kMinShare = 4;
+
+// A sequence's work. invalid: lengths that cannot be served.
+struct Seq {
+    int q0, c, ctx, tiles, row_tiles;
+    bool lost, invalid;
+    __device__ __forceinline__ long long cost(int nkv) const {
+        return static_cast<long long>(row_tiles) * nkv * (tiles + kUnitCost);
+    }
+};
+
+__device__ __forceinline__ Seq load_seq(const TreeArgs &a, int s, int log2_g) {
+    Seq q;
+    q.q0 = __ldg(a.cu_q_lens + s);
+    const int q1 = __ldg(a.cu_q_lens + s + 1);
+    q.ctx = __ldg(a.context_lens + s);
+    q.lost = q.q0 < 0 || q1 < q.q0 || q1 > a.total_q;  // its rows cannot be located
+    q.c = q.lost ? 0 : q1 - q.q0;
+    q.invalid = !q.lost && q.c > 0 && (q.c > a.max_q_len || q.ctx < q.c || q.ctx > a.max_context_len);
+    const bool work = !q.lost && !q.invalid && q.c > 0;
+    q.tiles = work ? (q.ctx + kBN - 1) / kBN : 0;
+    q.row_tiles = work ? ((q.c << log2_g) + kRows - 1) / kRows : 0;
+    return q;
+}
+
+// What a CTA works on at a time; the same in every thread.
 struct Unit {
     int s, kh, q0, c, ctx, base;
     int row0;    // first row (draft * G + head) of the tile
     int rows;    // live rows of the tile
     int per_copy, copies;
-    int t0, t1;  // keys of the partition
-    int tiles;
-    int part, parts;  // partition and number of partitions of this sequence
+    int t0, t1;  // its keys here
+    int tiles;   // and their tiles
+    int slot;    // workspace slot of a cut unit, -1 of a whole one
+};
+
+// All shares: share b is [b total / shares, (b + 1) total / shares) of the laid
+// out cost; the tiles of a unit at cost p lie at p + kUnitCost and behind.
+struct Shares {
+    long long total;
+    int shares;
+    __device__ __forceinline__ long long begin(int b) const { return total * b / shares; }
+};
+
+// Total cost (every thread of the block; `scratch` is shared memory for 9 values).
+template <int THREADS>
+__device__ __forceinline__ Shares count_shares(const TreeArgs &a, int log2_g, long long *scratch) {
+    long long sum = 0;
+    for (int s = threadIdx.x; s < a.num_seqs; s += THREADS) sum += load_seq(a, s, log2_g).cost(a.num_kv_heads);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    Shares r;
+    r.total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) r.total += scratch[w];
+    const long long most = r.total / a.min_share;
+    r.shares = static_cast<int>(most < 1 ? 1 : most < a.max_shares ? most : a.max_shares);
+    __syncthreads();
+    return r;
+}
+
+// The sequence that holds cost x < total, and the cost before it.
+template <int THREADS>
+__device__ __forceinline__ int find_seq(const TreeArgs &a, int log2_g, long long x, long long *scratch,
+                                        long long &before) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    long long done = 0;
+    for (int s0 = 0;; s0 += THREADS) {
+        const int s = s0 + threadIdx.x;
+        const long long cost = s < a.num_seqs ? load_seq(a, s, log2_g).cost(a.num_kv_heads) : 0;
+        long long inc = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) scratch[warp] = inc;
+        __syncthreads();
+        long long at = done;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            const long long v = scratch[w];
+            if (w < warp) at += v;
+            done += v;
+        }
+        at += inc;  // cost up to and with this sequence
+        const bool last = s0 + THREADS >= a.num_seqs;
+        const bool here = x < done || last;
+        __syncthreads();
+        if (here) {  // uniform: x lies in this chunk
+            if (s < a.num_seqs && x >= at - cost && x < at) {
+                scratch[0] = s;
+                scratch[1] = at - cost;
+            }
+            __syncthreads();
+            const int found = static_cast<int>(scratch[0]);
+            before = scratch[1];
+            __syncthreads();
+            return found;
+        }
+    }
+}
+
+// Tiles of a unit of n tiles at cost p before cost x.
+__device__ __forceinline__ int tiles_before(long long x, long long p, int n) {
+    const long long t = x - p - kUnitCost;
+    return t <= 0 ? 0 : t >= n ? n : static_cast<int>(t);
+}
+
+// Goes through the units of a share.
+struct Walk {
+    long long x0, x1, p;  // the share, and the cost of the next unit
+    int s, k, share;
+    Seq q;
+    __device__ __forceinline__ void start(const TreeArgs &a, const Shares &sh, int b, int seq, long long before,
+                                          int log2_g) {
+        share = b;
+        x0 = sh.begin(b);
+        x1 = sh.begin(b + 1);
+        s = seq;
+        q = load_seq(a, s, log2_g);
+        k = static_cast<int>((x0 - before) / (q.tiles + kUnitCost));
+        p = before + static_cast<long long>(k) * (q.tiles + kUnitCost);
+    }
+    __device__ __forceinline__ bool next(const TreeArgs &a, int log2_g, Unit &u) {
+        while (p < x1) {
+            while (k >= q.row_tiles * a.num_kv_heads) {
+                if (++s >= a.num_seqs) return false;
+                k = 0;
+                q = load_seq(a, s, log2_g);
+            }
+            const int tb = tiles_before(x0, p, q.tiles), te = tiles_before(x1, p, q.tiles);
+            const int kk = k;
+            p += q.tiles + kUnitCost;
+            ++k;
+            if (tb >= te) continue;
+            u.s = s;
+            u.kh = kk / q.row_tiles;
+            u.q0 = q.q0;
+            u.c = q.c;
+            u.ctx = q.ctx;
+            u.base = q.ctx - q.c;
+            u.row0 = (kk % q.row_tiles) * kRows;
+            u.rows = min(kRows, (q.c << log2_g) - u.row0);
+            u.per_copy = u.rows <= 32 ? 32 : u.rows <= 64 ? 64 : 128;
+            u.copies = kRows / u.per_copy;
+            u.t0 = tb * kBN;
+            u.t1 = min(q.ctx, te * kBN);
+            u.tiles = te - tb;
+            u.slot = tb > 0 ? 2 * share : te < q.tiles ? 2 * share + 1 : -1;
+            return true;
+        }
+        return false;
+    }
 };
 
 // Bits [start, start + 32) of a row's view of the context, position start being
@@ -196,12 +354,12 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t *mask, int c, int s
 // and elements that are not finite in the drafts' rows too; returns whether
 // there were any. F16: f16 elements, else bf16.
 template <int D, bool F16>
-__device__ __forceinline__ bool mend_v(uint32_t sv, int first, int end, bool zero_tail, int thread, int threads) {
+__device__ __forceinline__ bool mend_v(uint32_t sv, int first, int end, bool zero_tail, int thread) {
     constexpr int kChunks = D / 8;
     constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;
     bool found = false;
     const int last = zero_tail ? kBN : end;
-    for (int i = first * kChunks + thread; i < last * kChunks; i += threads) {
+    for (int i = first * kChunks + thread; i < last * kChunks; i += kSoftmaxWarps * 32) {
         const int r = i / kChunks, c16 = i % kChunks;
         const uint32_t at = sv + swz(kBN, r, c16);
         if (r >= end) {
@@ -232,127 +390,140 @@ __device__ __forceinline__ bool mend_v(uint32_t sv, int first, int end, bool zer
     return found;
 }
 
-// Softmax of this warp's rows over the partition: COLS keys of every tile (64
-// / copies). Leaves the reference maximum and the sum of the row (copy).
+// Softmax of this warp's rows over the unit's tiles: COLS keys of every tile (64
+// / copies). g0: tiles of the units before. Leaves the reference maximum and the
+// sum of the row (copy).
 template <int D, int MODE, int COLS>
 __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, TreeBars *bars, uint8_t *sm,
                                               uint32_t base, uint32_t tmem, float sl2, bool live, int draft,
-                                              int live_warps, float &m_out, float &l_out) {
+                                              uint32_t g0, int unit, float &m_out, float &l_out) {
     using L = TreeLayout<D, MODE>;
     constexpr bool kF16 = MODE == 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const bool idle = !__any_sync(0xffffffffu, live);  // no row in this warp: its weights are never read
     const int copy = COLS == 64 ? 0 : (warp * 32) / u.per_copy;
     const int col0 = copy * COLS;
     const uint32_t *mask = a.mask + static_cast<long long>(u.q0 + draft) * a.mask_words;
     float m = -INFINITY, l = 0.0f;
     for (int j = 0; j < u.tiles; ++j) {
+        const uint32_t g = g0 + j;
         const int kv0 = u.t0 + j * kBN;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[j & 1], (j >> 1) & 1))) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[g & 1], (g >> 1) & 1))) return false;
         tc_fence_after();
-        const uint32_t ts = tmem + (j & 1) * kBN + lane_base;
-        float x[COLS];
-        tmem_ldn<COLS>(ts + col0, x);
-        if constexpr (MODE == 2) {
-            const int slot = j % kNK;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_full[slot], (j / kNK) & 1))) return false;
-            const float4 *ks = reinterpret_cast<const float4 *>(sm + L::kKs + slot * kBN * 4 + col0 * 4);
-#pragma unroll
-            for (int i = 0; i < COLS / 4; ++i) {
-                const float4 k4 = ks[i];
-                x[4 * i] *= k4.x * sl2;
-                x[4 * i + 1] *= k4.y * sl2;
-                x[4 * i + 2] *= k4.z * sl2;
-                x[4 * i + 3] *= k4.w * sl2;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->k_empty[slot]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < COLS; ++i) x[i] *= sl2;
-        }
         const bool special = kv0 + kBN > u.base;  // holds drafts, or keys past the end
-        if (special) {
-#pragma unroll
-            for (int h = 0; h < (COLS + 31) / 32; ++h) {
-                const uint32_t vis = live ? visible32(mask, u.c, kv0 + col0 + 32 * h, u.base) : 0u;
-#pragma unroll
-                for (int i = 0; i < (COLS < 32 ? COLS : 32); ++i)
-                    if (!((vis >> i) & 1u)) x[32 * h + i] = -INFINITY;
+        if (idle) {
+            if constexpr (MODE == 2) {
+                if (lane == 0) mbar_arrive(&bars->k_empty[g % kNK]);
             }
-        }
-        float m8[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m8[k] = x[k];
-#pragma unroll
-        for (int i = 8; i < COLS; ++i) m8[i & 7] = fmaxf(m8[i & 7], x[i]);
-        const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-        float alpha = 1.0f;
-        bool rescale = false;
-        if (j == 0) {
-            m = mx;
         } else {
-            const bool grow = mx > m + 8.0f;
-            rescale = __any_sync(0xffffffffu, grow);
-            if (grow) {
-                alpha = fast_exp2(m - mx);
-                m = mx;
-                l *= alpha;
+            const uint32_t ts = tmem + (g & 1) * kBN + lane_base;
+            float x[COLS];
+            tmem_ldn<COLS>(ts + col0, x);
+            if constexpr (MODE == 2) {
+                const int slot = g % kNK;
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_full[slot], (g / kNK) & 1))) return false;
+                const float4 *ks = reinterpret_cast<const float4 *>(sm + L::kKs + slot * kBN * 4 + col0 * 4);
+#pragma unroll
+                for (int i = 0; i < COLS / 4; ++i) {
+                    const float4 k4 = ks[i];
+                    x[4 * i] *= k4.x * sl2;
+                    x[4 * i + 1] *= k4.y * sl2;
+                    x[4 * i + 2] *= k4.z * sl2;
+                    x[4 * i + 3] *= k4.w * sl2;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < COLS; ++i) x[i] *= sl2;
             }
-        }
-        const float ref = m == -INFINITY ? 0.0f : m;  // nothing seen yet: weights exp2(-inf) = 0
-        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (special) {
 #pragma unroll
-        for (int g = 0; g < COLS / 16; ++g) {
-            uint32_t w[8];
+                for (int h = 0; h < (COLS + 31) / 32; ++h) {
+                    const uint32_t vis = live ? visible32(mask, u.c, kv0 + col0 + 32 * h, u.base) : 0u;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p0 = fast_exp2(x[16 * g + 2 * i] - ref), p1 = fast_exp2(x[16 * g + 2 * i + 1] - ref);
-                if constexpr (kF16) {
-                    w[i] = pack_f16(p0, p1);
-                    l4[i & 3] = fma_f16x2_acc(w[i], 0x3C003C00u, l4[i & 3]);
-                } else {
-                    w[i] = pack_bf16(p0, p1);
-                    l4[i & 3] = fma_bf16x2_acc(w[i], 0x3F803F80u, l4[i & 3]);
+                    for (int i = 0; i < (COLS < 32 ? COLS : 32); ++i)
+                        if (!((vis >> i) & 1u)) x[32 * h + i] = -INFINITY;
                 }
             }
-            tmem_st8(ts + col0 / 2 + 8 * g, w);
-        }
-        if constexpr (COLS < 64) {  // the other copies' keys
-            const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            float m8[8];
 #pragma unroll
-            for (int g = COLS / 16; g < 4; ++g) tmem_st8(ts + ((col0 / 2 + 8 * g) & 31), zero);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        if (rescale) {  // S(j) done implies P V(j - 2) done: the next phase is P V(j - 1)
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (j - 1) & 1))) return false;
-            tc_fence_after();
+            for (int k = 0; k < 8; ++k) m8[k] = x[k];
 #pragma unroll
-            for (int ch = 0; ch < D / 32; ++ch) {
-                float v[32];
-                tmem_ld32(tmem + 128 + lane_base + ch * 32, v);
+            for (int i = 8; i < COLS; ++i) m8[i & 7] = fmaxf(m8[i & 7], x[i]);
+            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+            float alpha = 1.0f;
+            bool rescale = false;
+            if (j == 0) {
+                m = mx;
+            } else {
+                const bool grow = mx > m + 8.0f;
+                rescale = __any_sync(0xffffffffu, grow);
+                if (grow) {
+                    alpha = fast_exp2(m - mx);
+                    m = mx;
+                    l *= alpha;
+                }
+            }
+            const float ref = m == -INFINITY ? 0.0f : m;  // nothing seen yet: weights exp2(-inf) = 0
+            float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= alpha;
-                tmem_st32_async(tmem + 128 + lane_base + ch * 32, v);
+            for (int h = 0; h < COLS / 16; ++h) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p0 = fast_exp2(x[16 * h + 2 * i] - ref), p1 = fast_exp2(x[16 * h + 2 * i + 1] - ref);
+                    if constexpr (kF16) {
+                        w[i] = pack_f16(p0, p1);
+                        l4[i & 3] = fma_f16x2_acc(w[i], 0x3C003C00u, l4[i & 3]);
+                    } else {
+                        w[i] = pack_bf16(p0, p1);
+                        l4[i & 3] = fma_bf16x2_acc(w[i], 0x3F803F80u, l4[i & 3]);
+                    }
+                }
+                tmem_st8(ts + col0 / 2 + 8 * h, w);
+            }
+            if constexpr (COLS < 64) {  // the other copies' keys
+                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int h = COLS / 16; h < 4; ++h) tmem_st8(ts + ((col0 / 2 + 8 * h) & 31), zero);
+            }
+            l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            if constexpr (MODE == 2) {
+                // here, behind instructions that used every lane's scales: released right
+                // after the loads, the slot was refilled under lanes still reading it
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->k_empty[g % kNK]);
+            }
+            if (rescale) {  // S(j) done implies P V(j - 2) done: the next phase is P V(j - 1)
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (g - 1) & 1))) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    float v[32];
+                    tmem_ld32(tmem + 128 + lane_base + ch * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= alpha;
+                    tmem_st32_async(tmem + 128 + lane_base + ch * 32, v);
+                }
             }
         }
         if (special) {
-            const int slot = j % kNV;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[slot], (j / kNV) & 1))) return false;
+            const int slot = g % kNV;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[slot], (g / kNV) & 1))) return false;
             const int first = max(0, u.base - kv0), end = min(kBN, u.ctx - kv0);
-            if (mend_v<D, kF16>(base + L::kV + slot * L::kVSlot, first, end, MODE == 0, threadIdx.x, 32 * live_warps))
-                bars->nonfinite = 1;
+            if (mend_v<D, kF16>(base + L::kV + slot * L::kVSlot, first, end, MODE == 0, threadIdx.x))
+                bars->nonfinite[unit & 1] = 1;
             fence_proxy_async_smem();
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[j & 1]);
+        if (lane == 0) mbar_arrive(&bars->p_full[g & 1]);
     }
-    // its own barrier: pv_done may be one or two phases further by now, and a
-    // parity cannot tell which
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_done, 0))) return false;
+    // a barrier of its own: pv_done may be one or two phases further by now, and
+    // a parity cannot tell which
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_done, unit & 1))) return false;
     tc_fence_after();
     m_out = m;
     l_out = l;
@@ -394,37 +565,88 @@ __device__ __forceinline__ void add_nonfinite(const TreeArgs &a, const Unit &u, 
     for (int i = 0; i < N; ++i) v[i] = t[i];
 }
 
-// N result elements from column col of a row: bf16 output, or a partition's
-// binary32 partial.
-template <int D, int N>
-__device__ __forceinline__ void put(const TreeArgs &a, const Unit &u, int draft, int head, int col, const float *v) {
-    const long long nq = a.num_q_heads;
-    if (u.parts == 1) {
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + ((u.q0 + draft) * nq + head) * D + col;
+// Results of a unit: the copies joined, normalised, written through shared
+// memory so that lanes write neighbouring elements: bf16 output, or the
+// binary32 partial (and maximum and sum) of a cut unit.
+template <int D, int MODE>
+__device__ __forceinline__ void write_unit(const TreeArgs &a, const Unit &u, TreeBars *bars, uint8_t *sm, uint32_t tmem,
+                                           int unit, int log2_g, bool ok, float m, float l) {
+    using L = TreeLayout<D, MODE>;
+    constexpr int kCols = L::kOutCols, kStride = kCols + 4;
+    const int tid = threadIdx.x, G = 1 << log2_g;
+    const int r = tid & (u.per_copy - 1);
+    float *ml = reinterpret_cast<float *>(sm + L::kMl);
+    float *o = reinterpret_cast<float *>(sm + L::kQ);
+    ml[tid] = m;
+    ml[kRows + tid] = ok ? l : 0.0f;
+    named_sync(1, kSoftmaxWarps * 32);  // (also: the flags are complete)
+    const bool nonfinite = bars->nonfinite[unit & 1] != 0, bad = bars->bad[unit & 1] != 0;
+    float top = -INFINITY, sum = 0.0f;
+    for (int k = 0; k < u.copies; ++k) top = fmaxf(top, ml[k * u.per_copy + r]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    for (int k = 0; k < u.copies; ++k)
+        sum = fmaf(fast_exp2(ml[k * u.per_copy + r] - ref), ml[kRows + k * u.per_copy + r], sum);
+    // a copy (or row) that saw nothing, and a bad unit, contribute zeros whatever O holds
+    const bool drop = l == 0.0f || sum == 0.0f || bad || !ok;
+    const float f = drop ? 0.0f : fast_exp2(m - ref) * ((MODE == 1 ? __ldg(a.v_scale + u.kh) : 1.0f) / sum);
+    const long long slot_rows = min(static_cast<long long>(kRows), static_cast<long long>(a.max_q_len) << log2_g);
+    if (u.slot >= 0 && tid < u.rows)
+        *reinterpret_cast<float2 *>(a.part_ml + (u.slot * slot_rows + tid) * 2) = make_float2(top, bad ? -1.0f : sum);
+    const uint32_t tmem_o = tmem + 128 + (static_cast<uint32_t>((tid >> 5) * 32) << 16);
+#pragma unroll 1
+    for (int ch = 0; ch < D / kCols; ++ch) {
+        float v[kCols];
+        tmem_ldn<kCols>(tmem_o + ch * kCols, v);
 #pragma unroll
-        for (int i = 0; i < N; i += 8)
-            *reinterpret_cast<uint4 *>(dst + i) =
-                make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
-                           pack_bf16(v[i + 6], v[i + 7]));
-    } else {
-        const long long prow = (static_cast<long long>(u.s) * a.max_q_len + draft) * nq + head;
-        float *dst = a.part_o + (prow * a.num_partitions + u.part) * D + col;
+        for (int i = 0; i < kCols; i += 4)
+            *reinterpret_cast<float4 *>(o + tid * kStride + i) =
+                drop ? make_float4(0, 0, 0, 0) : make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
+        named_sync(1, kSoftmaxWarps * 32);
+        constexpr int kPer = kCols / 8;  // 8 columns a thread
+        for (int i = tid; i < u.rows * kPer; i += kSoftmaxWarps * 32) {
+            const int rr = i / kPer, col = (i % kPer) * 8;
+            const int row = u.row0 + rr, draft = row >> log2_g, head = u.kh * G + (row & (G - 1));
+            float x[8];
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-            *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int e = 0; e < 8; e += 4) {
+                float4 y = *reinterpret_cast<const float4 *>(o + rr * kStride + col + e);
+                for (int k = 1; k < u.copies; ++k) {
+                    const float4 z = *reinterpret_cast<const float4 *>(o + (k * u.per_copy + rr) * kStride + col + e);
+                    y.x += z.x;
+                    y.y += z.y;
+                    y.z += z.z;
+                    y.w += z.w;
+                }
+                x[e] = y.x;
+                x[e + 1] = y.y;
+                x[e + 2] = y.z;
+                x[e + 3] = y.w;
+            }
+            if (nonfinite && !bad) add_nonfinite<D, MODE>(a, u, draft, ch * kCols + col, x);
+            if (u.slot < 0) {
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                                     (static_cast<long long>(u.q0 + draft) * a.num_q_heads + head) * D + ch * kCols + col;
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                             pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            } else {
+                float *dst = a.part_o + (u.slot * slot_rows + rr) * D + ch * kCols + col;
+                *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            }
+        }
+        named_sync(1, kSoftmaxWarps * 32);
     }
-}
-
-__device__ __forceinline__ void put_ml(const TreeArgs &a, const Unit &u, int draft, int head, float m, float l) {
-    if (u.parts == 1) return;
-    const long long prow = (static_cast<long long>(u.s) * a.max_q_len + draft) * a.num_q_heads + head;
-    *reinterpret_cast<float2 *>(a.part_ml + (prow * a.num_partitions + u.part) * 2) = make_float2(m, l);
+    if (tid == 0) {
+        if (bad) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
+        bars->nonfinite[unit & 1] = 0;  // read by everyone above; next used two units on
+        bars->bad[unit & 1] = 0;
+    }
 }
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
-    tree_kernel(const __grid_constant__ TreeArgs a, int log2_bs, int log2_g, int row_tiles,
-                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    tree_kernel(const __grid_constant__ TreeArgs a, int log2_bs, int log2_g, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v) {
     using L = TreeLayout<D, MODE>;
     constexpr bool kFp8 = MODE != 0;
     constexpr int kThreads = tree_threads<MODE>();
@@ -436,62 +658,13 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = 1 << log2_g, bs = a.block_size;
 
-    // ------------------------------------------------ the unit, checked
-    Unit u;
-    int b = blockIdx.x;
-    const int rt = b % row_tiles;
-    b /= row_tiles;
-    u.kh = b % a.num_kv_heads;
-    b /= a.num_kv_heads;
-    u.s = b % a.num_seqs;
-    u.part = b / a.num_seqs;
-    u.q0 = __ldg(a.cu_q_lens + u.s);
-    const int q1 = __ldg(a.cu_q_lens + u.s + 1);
-    u.ctx = __ldg(a.context_lens + u.s);
-    if (u.q0 < 0 || q1 < u.q0 || q1 > a.total_q) {
-        if (tid == 0 && rt == 0 && u.kh == 0 && u.part == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
-        return;  // no row of this sequence can be located safely
-    }
-    u.c = q1 - u.q0;
-    u.row0 = rt * kRows;
-    if (u.row0 >= u.c << log2_g) return;
-    if (u.c > a.max_q_len || u.ctx < u.c || u.ctx > a.max_context_len) {
-        if (u.part == 0) {  // zeros for this KV head's rows, whatever the chunk's length
-            const long long n = static_cast<long long>(u.c) << log2_g;
-            for (long long i = rt * kThreads + tid; i < n * (D / 8); i += static_cast<long long>(row_tiles) * kThreads) {
-                const long long r = i / (D / 8);
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                     ((u.q0 + (r >> log2_g)) * a.num_q_heads + u.kh * G + (r & (G - 1))) * D;
-                *reinterpret_cast<uint4 *>(dst + (i % (D / 8)) * 8) = make_uint4(0, 0, 0, 0);
-            }
-            if (tid == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
-        }
-        return;
-    }
-    u.base = u.ctx - u.c;
-    u.parts = a.partition_tokens > 0 ? (u.ctx + a.partition_tokens - 1) / a.partition_tokens : 1;
-    if (u.part >= u.parts) return;
-    u.t0 = u.part * a.partition_tokens;
-    u.t1 = u.parts > 1 ? min(u.ctx, u.t0 + a.partition_tokens) : u.ctx;
-    u.tiles = (u.t1 - u.t0 + kBN - 1) / kBN;
-    u.rows = min(kRows, (u.c << log2_g) - u.row0);
-    u.per_copy = u.rows <= 32 ? 32 : u.rows <= 64 ? 64 : 128;
-    u.copies = kRows / u.per_copy;
-    const int live_warps = u.copies > 1 ? 4 : (u.rows + 31) / 32;
-    const int32_t *table = a.block_tables + static_cast<long long>(u.s) * a.max_blocks_per_seq;
-    bool bad = false;
-    for (int i = (u.t0 >> log2_bs) + tid; i <= (u.t1 - 1) >> log2_bs; i += kThreads) {
-        const int id = __ldg(table + i);
-        bad |= id < 0 || id >= a.num_blocks;
-    }
-
     // ------------------------------------------------ setup
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&bars->tmem), kTmemCols);
     if (tid == 0) {
         mbar_init(&bars->q_full, kSoftmaxWarps * 32);
         for (int i = 0; i < kNK; ++i) {
             mbar_init(&bars->k_full[i], 1);
-            mbar_init(&bars->k_empty[i], MODE == 2 ? 1 + live_warps : 1);  // the scales are read by the softmax
+            mbar_init(&bars->k_empty[i], MODE == 2 ? 1 + kSoftmaxWarps : 1);  // the scales are read by the softmax
         }
         for (int i = 0; i < kNV; ++i) {
             mbar_init(&bars->v_full[i], kFp8 ? kConvWarps : 1);
@@ -501,253 +674,211 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_full[i], live_warps);
+            mbar_init(&bars->p_full[i], kSoftmaxWarps);
+            bars->nonfinite[i] = 0;
+            bars->bad[i] = 0;
         }
+        bars->failed = 0;
         mbar_init(&bars->pv_done, 1);
         mbar_init(&bars->o_done, 1);
         mbar_init(&bars->drained, 1);
-        bars->nonfinite = 0;
         fence_barrier_init();
     }
+    // sequences that cannot be served: reported, and zeros where their rows can be located
+    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
+        const Seq q = load_seq(a, s, log2_g);
+        if ((q.lost || q.invalid) && tid == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
+        if (q.invalid) {
+            const long long n = static_cast<long long>(q.c) * a.num_q_heads * (D / 8);
+            uint4 *dst = static_cast<uint4 *>(a.out) + static_cast<long long>(q.q0) * a.num_q_heads * (D / 8);
+            for (long long i = tid; i < n; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    const Shares sh = count_shares<kThreads>(a, log2_g, bars->scan);
     tc_fence_before();
-    bad = __syncthreads_or(bad);
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
+    const int share = blockIdx.x;
+    const bool work = sh.total > 0 && share < sh.shares;
+    Walk walk;
+    Unit u;
+    uint32_t g = 0;  // tiles of the units before
+    if (work) {
+        long long before;
+        const int s = find_seq<kThreads>(a, log2_g, sh.begin(share), bars->scan, before);
+        walk.start(a, sh, share, s, before, log2_g);
+    }
 
-    // this softmax thread's row: tile position warp * 32 + lane, copy position / per_copy
-    const int pos = tid & (kRows - 1);
-    const int r = pos & (u.per_copy - 1);
-    const bool live = r < u.rows;
-    const int row = u.row0 + (live ? r : 0);
-    const int draft = row >> log2_g, head = u.kh * G + (row & (G - 1));
-
-    if (bad) {  // zeros, or partials that the join turns into zeros
-        if (warp < kSoftmaxWarps && live && pos < u.per_copy) {
-            const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int i = 0; i < D; i += 8) put<D, 8>(a, u, draft, head, i, zero);
-            put_ml(a, u, draft, head, -INFINITY, -1.0f);
-        }
-        if (tid == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
+    if (!work) {
+        // more CTAs than shares
     } else if (warp < kSoftmaxWarps) {
         // ================================================ softmax
-        float sl2 = a.scale * kLog2e;
-        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q);
-        const uint4 *qrow = reinterpret_cast<const uint4 *>(
-            qp + (static_cast<long long>(u.q0 + draft) * a.num_q_heads + head) * D);
-        constexpr int kChunks = D / 8;
-        if constexpr (!kFp8) {
-            for (int i = tid; i < kRows * kChunks; i += kRows) {
-                const int p = i / kChunks, c16 = i % kChunks;
-                const int pr = p & (u.per_copy - 1);
-                const bool ok = pr < u.rows;
-                const int rr = u.row0 + (ok ? pr : 0);
-                const long long e = (static_cast<long long>(u.q0 + (rr >> log2_g)) * a.num_q_heads + u.kh * G +
-                                     (rr & (G - 1))) * D + c16 * 8;
-                cp_async16(base + L::kQ + swz(kRows, p, c16), qp + e, ok ? 16u : 0u);
-            }
-            cp_async_commit();
-            cp_async_wait0();
-        } else {
-            uint4 qv[kChunks];
-            float amax = 0.0f;
-#pragma unroll
-            for (int c16 = 0; c16 < kChunks; ++c16) {
-                qv[c16] = live ? __ldg(qrow + c16) : make_uint4(0, 0, 0, 0);
-                const uint32_t w[4] = {qv[c16].x, qv[c16].y, qv[c16].z, qv[c16].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
-            }
-            // amax < 2^e; times 2^kq it lies in [2^7, 2^8). kq is capped at 60
-            // so that 2^-kq times the softmax scale stays normal: rows that
-            // small have scores of zero to binary32 against any finite key.
-            const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 126;
-            const int kq = min(60, 8 - e);
-            const float qs = __int_as_float((kq + 127) << 23);
-            sl2 *= __int_as_float((127 - kq) << 23);
-            if (MODE == 1) sl2 *= __ldg(a.k_scale + u.kh);
-            if (!(amax <= 3.4e38f)) sl2 = __int_as_float(0x7FC00000);  // an infinite query: E4M3 has none
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {  // 16 elements: one chunk of hi and of lo
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint4 v4 = qv[2 * c + k / 4];
-                    const uint32_t wv[4] = {v4.x, v4.y, v4.z, v4.w};
-                    const uint32_t w = wv[k & 3];
-                    const float x = bf16lo(w) * qs, y = bf16hi(w) * qs;
-                    const uint16_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-                    const float2 hf = e4m3x2_to_float2(h);
-                    const uint16_t o =
-                        __nv_cvt_float2_to_fp8x2(make_float2(x - hf.x, y - hf.y), __NV_SATFINITE, __NV_E4M3);
-                    if (k & 1) {
-                        hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
-                        lo[k >> 1] |= static_cast<uint32_t>(o) << 16;
-                    } else {
-                        hi[k >> 1] = h;
-                        lo[k >> 1] = o;
-                    }
+        for (int unit = 0; walk.next(a, log2_g, u); ++unit) {
+            // this thread's row: copy tid / per_copy
+            const int r = tid & (u.per_copy - 1);
+            const bool live = r < u.rows;
+            const int row = u.row0 + (live ? r : 0);
+            const int draft = row >> log2_g, head = u.kh * G + (row & (G - 1));
+            const int32_t *table = a.block_tables + static_cast<long long>(u.s) * a.max_blocks_per_seq;
+            float sl2 = a.scale * kLog2e;
+            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q);
+            constexpr int kChunks = D / 8;
+            if constexpr (!kFp8) {
+                for (int i = tid; i < kRows * kChunks; i += kRows) {
+                    const int p = i / kChunks, c16 = i % kChunks;
+                    const int pr = p & (u.per_copy - 1);
+                    const bool ok = pr < u.rows;
+                    const int rr = u.row0 + (ok ? pr : 0);
+                    const long long e = (static_cast<long long>(u.q0 + (rr >> log2_g)) * a.num_q_heads + u.kh * G +
+                                         (rr & (G - 1))) * D + c16 * 8;
+                    cp_async16(base + L::kQ + swz(kRows, p, c16), qp + e, ok ? 16u : 0u);
                 }
-                const uint32_t at = base + L::kQ + swz8<D>(pos, c);
-                st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                st_shared16(at + kRows * D, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-            }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&bars->q_full);
-
-        bool ok = true;
-        float m = -INFINITY, l = 0.0f;
-        if (warp < live_warps) {
-            if (u.copies == 4)
-                ok = softmax_tiles<D, MODE, 16>(a, u, bars, sm, base, tmem, sl2, live, draft, live_warps, m, l);
-            else if (u.copies == 2)
-                ok = softmax_tiles<D, MODE, 32>(a, u, bars, sm, base, tmem, sl2, live, draft, live_warps, m, l);
-            else
-                ok = softmax_tiles<D, MODE, 64>(a, u, bars, sm, base, tmem, sl2, live, draft, live_warps, m, l);
-        }
-        if (!ok && lane == 0) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
-        const float vsc = MODE == 1 ? __ldg(a.v_scale + u.kh) : 1.0f;
-        const uint32_t tmem_o = tmem + 128 + (static_cast<uint32_t>(warp * 32) << 16);
-        named_sync(1, kSoftmaxWarps * 32);  // (also: nonfinite is complete)
-        const bool nonfinite = bars->nonfinite != 0;
-        if (u.copies == 1) {
-            if (warp < live_warps && ok) {
-                const float inv = l == 0.0f ? 0.0f : vsc / l;
+                cp_async_commit();
+                cp_async_wait0();
+            } else {
+                const uint4 *qrow = reinterpret_cast<const uint4 *>(
+                    qp + (static_cast<long long>(u.q0 + draft) * a.num_q_heads + head) * D);
+                uint4 qv[kChunks];
+                float amax = 0.0f;
 #pragma unroll
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    float v[32];
-                    tmem_ld32(tmem_o + ch * 32, v);
-                    if (live) {
+                for (int c16 = 0; c16 < kChunks; ++c16) {
+                    qv[c16] = live ? __ldg(qrow + c16) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {qv[c16].x, qv[c16].y, qv[c16].z, qv[c16].w};
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = l == 0.0f ? 0.0f : v[i] * inv;
-                        if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, ch * 32, v);
-                        put<D, 32>(a, u, draft, head, ch * 32, v);
-                    }
+                    for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
                 }
-                if (live) put_ml(a, u, draft, head, m, l);
-            }
-        } else {
-            // join the copies: their sums to one maximum, their O through shared memory
-            float *ml = reinterpret_cast<float *>(sm + L::kMl);
-            float *o = reinterpret_cast<float *>(sm);  // [kRows][D + 4], over Q and the rings
-            ml[pos] = m;
-            ml[kRows + pos] = l;
-            named_sync(1, kSoftmaxWarps * 32);
-            float top = -INFINITY, sum = 0.0f;
-            for (int k = 0; k < u.copies; ++k) top = fmaxf(top, ml[k * u.per_copy + r]);
-            const float ref = top == -INFINITY ? 0.0f : top;
-            for (int k = 0; k < u.copies; ++k)
-                sum = fmaf(fast_exp2(ml[k * u.per_copy + r] - ref), ml[kRows + k * u.per_copy + r], sum);
-            const float w = m == -INFINITY ? 0.0f : fast_exp2(m - ref);
+                // amax < 2^e; times 2^kq it lies in [2^7, 2^8). kq is capped at 60
+                // so that 2^-kq times the softmax scale stays normal: rows that
+                // small have scores of zero to binary32 against any finite key.
+                const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 126;
+                const int kq = min(60, 8 - e);
+                const float qs = __int_as_float((kq + 127) << 23);
+                sl2 *= __int_as_float((127 - kq) << 23);
+                if (MODE == 1) sl2 *= __ldg(a.k_scale + u.kh);
+                if (!(amax <= 3.4e38f)) sl2 = __int_as_float(0x7FC00000);  // an infinite query: E4M3 has none
 #pragma unroll
-            for (int ch = 0; ch < D / 32; ++ch) {
-                float v[32];
-                tmem_ld32(tmem_o + ch * 32, v);
+                for (int c = 0; c < D / 16; ++c) {  // 16 elements: one chunk of hi and of lo
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4 *>(o + pos * (D + 4) + ch * 32 + i) =
-                        l == 0.0f ? make_float4(0, 0, 0, 0)
-                                  : make_float4(v[i] * w, v[i + 1] * w, v[i + 2] * w, v[i + 3] * w);
-            }
-            named_sync(1, kSoftmaxWarps * 32);
-            if (live && ok) {
-                // this thread: D / copies columns of its row
-                const float inv = sum == 0.0f ? 0.0f : vsc / sum;
-                const int width = D / u.copies, first = (pos / u.per_copy) * width;
-                for (int c8 = 0; c8 < width; c8 += 8) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        float4 acc = *reinterpret_cast<const float4 *>(o + r * (D + 4) + first + c8 + i);
-                        for (int k = 1; k < u.copies; ++k) {
-                            const float4 x =
-                                *reinterpret_cast<const float4 *>(o + (k * u.per_copy + r) * (D + 4) + first + c8 + i);
-                            acc.x += x.x;
-                            acc.y += x.y;
-                            acc.z += x.z;
-                            acc.w += x.w;
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 v4 = qv[2 * c + k / 4];
+                        const uint32_t wv[4] = {v4.x, v4.y, v4.z, v4.w};
+                        const uint32_t w = wv[k & 3];
+                        const float x = bf16lo(w) * qs, y = bf16hi(w) * qs;
+                        const uint16_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+                        const float2 hf = e4m3x2_to_float2(h);
+                        const uint16_t o =
+                            __nv_cvt_float2_to_fp8x2(make_float2(x - hf.x, y - hf.y), __NV_SATFINITE, __NV_E4M3);
+                        if (k & 1) {
+                            hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
+                            lo[k >> 1] |= static_cast<uint32_t>(o) << 16;
+                        } else {
+                            hi[k >> 1] = h;
+                            lo[k >> 1] = o;
                         }
-                        v[i] = acc.x * inv;
-                        v[i + 1] = acc.y * inv;
-                        v[i + 2] = acc.z * inv;
-                        v[i + 3] = acc.w * inv;
                     }
-                    if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, first + c8, v);
-                    put<D, 8>(a, u, draft, head, first + c8, v);
+                    const uint32_t at = base + L::kQ + swz8<D>(tid, c);
+                    st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    st_shared16(at + kRows * D, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                 }
-                if (pos < u.per_copy) put_ml(a, u, draft, head, top, sum);
             }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars->q_full);
+            // the producer copies block 0 in place of an id outside the pool; the results become zeros
+            for (int i = (u.t0 >> log2_bs) + tid; i <= (u.t1 - 1) >> log2_bs; i += kRows) {
+                const int id = __ldg(table + i);
+                if (id < 0 || id >= a.num_blocks) bars->bad[unit & 1] = 1;
+            }
+            float m = -INFINITY, l = 0.0f;
+            bool ok;
+            if (u.copies == 4)
+                ok = softmax_tiles<D, MODE, 16>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
+            else if (u.copies == 2)
+                ok = softmax_tiles<D, MODE, 32>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
+            else
+                ok = softmax_tiles<D, MODE, 64>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
+            if (!ok && lane == 0) {
+                set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
+                bars->failed = 1;
+            }
+            g += u.tiles;
+            write_unit<D, MODE>(a, u, bars, sm, tmem, unit, log2_g, ok, m, l);
+            if (bars->failed) break;  // written before a barrier of write_unit: the same for all
         }
         __syncwarp();
     } else if (warp == kProducerWarp) {
         // ================================================ producer
         constexpr int kHalves = D / 64;
-        int issued_k = 0, issued_v = 0;
-        // block ids, 32 at a time, the next 32 already loading
-        const int first_blk = u.t0 >> log2_bs, last_blk = (u.t1 - 1) >> log2_bs;
-        int win = first_blk;
-        int id = __ldg(table + min(win + lane, last_blk)), id_next = __ldg(table + min(win + 32 + lane, last_blk));
         bool ok = true;
-        for (int j = 0; j < u.tiles; ++j) {
-            const int kv0 = u.t0 + j * kBN;
-            const int blk0 = kv0 >> log2_bs;
-            if (blk0 >= win + 32) {
-                win += 32;
-                id = id_next;
-                id_next = __ldg(table + min(win + 32 + lane, last_blk));
-            }
-            const int run = min(bs, kBN);  // rows per copy
-            const int n = bs >= kBN ? 1 : (min(kv0 + kBN, u.t1) - kv0 + bs - 1) >> log2_bs;
-            // lane i handles block i of the tile (bf16: lane 2 i + half)
-            const int bi = kFp8 ? lane : lane / kHalves;
-            const int half = kFp8 ? 0 : lane % kHalves;
-            const int blk = __shfl_sync(0xffffffffu, id, (blk0 - win + min(bi, n - 1)) & 31);
-            const long long prow = (static_cast<long long>(blk) * a.num_kv_heads + u.kh) * bs + (kv0 & (bs - 1));
-            const bool mine = bi < n;
-            auto stage = [&](bool is_k) -> bool {
-                const int slot = is_k ? j % kNK : j % kNV, use = is_k ? j / kNK : j / kNV;
-                uint64_t *empty = is_k ? &bars->k_empty[slot] : kFp8 ? &bars->raw_empty[slot] : &bars->v_empty[slot];
-                uint64_t *full = is_k ? &bars->k_full[slot] : kFp8 ? &bars->raw_full[slot] : &bars->v_full[slot];
-                if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (use - 1) & 1))) return false;
-                const uint32_t bytes = static_cast<uint32_t>(n * run) * (D * (kFp8 ? 1 : 2) + (MODE == 2 ? 4 : 0));
-                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-                __syncwarp();
-                if (mine) {
-                    if constexpr (!kFp8) {
-                        const uint32_t dst = base + (is_k ? L::kK + slot * L::kKSlot : L::kV + slot * L::kVSlot);
-                        tma_load_2d(dst + half * kBN * 128 + bi * run * 128, is_k ? &map_k : &map_v, half * 64,
-                                    static_cast<int>(prow), full);
-                    } else {
-                        if (is_k)
-                            tma_load_2d(base + L::kK + slot * L::kKSlot + bi * run * D, &map_k, 0,
-                                        static_cast<int>(prow), full);
-                        else
-                            bulk_g2s(sm + L::kRaw + slot * L::kRawSlot + bi * run * D,
-                                     static_cast<const uint8_t *>(a.v_cache) + prow * D, run * D, full);
-                        if constexpr (MODE == 2)
-                            bulk_g2s(sm + (is_k ? L::kKs : L::kVs) + slot * kBN * 4 + bi * run * 4,
-                                     (is_k ? a.k_scale : a.v_scale) + prow, run * 4, full);
-                    }
+        uint32_t issued_k = 0, issued_v = 0;
+        while (ok && walk.next(a, log2_g, u)) {
+            const int32_t *table = a.block_tables + static_cast<long long>(u.s) * a.max_blocks_per_seq;
+            // block ids, 32 at a time, the next 32 already loading
+            const int last_blk = (u.t1 - 1) >> log2_bs;
+            int win = u.t0 >> log2_bs;
+            int id = __ldg(table + min(win + lane, last_blk)), id_next = __ldg(table + min(win + 32 + lane, last_blk));
+            for (int j = 0; j < u.tiles; ++j) {
+                const int kv0 = u.t0 + j * kBN;
+                const int blk0 = kv0 >> log2_bs;
+                if (blk0 >= win + 32) {
+                    win += 32;
+                    id = id_next;
+                    id_next = __ldg(table + min(win + 32 + lane, last_blk));
                 }
-                return true;
-            };
-            if (!stage(true)) {
-                ok = false;
-                break;
+                const int run = min(bs, kBN);  // rows per copy
+                const int n = bs >= kBN ? 1 : (min(kv0 + kBN, u.t1) - kv0 + bs - 1) >> log2_bs;
+                // lane i handles block i of the tile (bf16: lane kHalves i + half)
+                const int bi = kFp8 ? lane : lane / kHalves;
+                const int half = kFp8 ? 0 : lane % kHalves;
+                int blk = __shfl_sync(0xffffffffu, id, (blk0 - win + min(bi, n - 1)) & 31);
+                if (blk < 0 || blk >= a.num_blocks) blk = 0;
+                const long long prow = (static_cast<long long>(blk) * a.num_kv_heads + u.kh) * bs + (kv0 & (bs - 1));
+                const bool mine = bi < n;
+                const uint32_t t = g + j;
+                auto stage = [&](bool is_k) -> bool {
+                    const uint32_t slot = is_k ? t % kNK : t % kNV, use = is_k ? t / kNK : t / kNV;
+                    uint64_t *empty = is_k ? &bars->k_empty[slot] : kFp8 ? &bars->raw_empty[slot] : &bars->v_empty[slot];
+                    uint64_t *full = is_k ? &bars->k_full[slot] : kFp8 ? &bars->raw_full[slot] : &bars->v_full[slot];
+                    if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (use - 1) & 1))) return false;
+                    const uint32_t bytes = static_cast<uint32_t>(n * run) * (D * (kFp8 ? 1 : 2) + (MODE == 2 ? 4 : 0));
+                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                    __syncwarp();
+                    if (mine) {
+                        if constexpr (!kFp8) {
+                            const uint32_t dst = base + (is_k ? L::kK + slot * L::kKSlot : L::kV + slot * L::kVSlot);
+                            tma_load_2d(dst + half * kBN * 128 + bi * run * 128, is_k ? &map_k : &map_v, half * 64,
+                                        static_cast<int>(prow), full);
+                        } else {
+                            if (is_k)
+                                tma_load_2d(base + L::kK + slot * L::kKSlot + bi * run * D, &map_k, 0,
+                                            static_cast<int>(prow), full);
+                            else
+                                bulk_g2s(sm + L::kRaw + slot * L::kRawSlot + bi * run * D,
+                                         static_cast<const uint8_t *>(a.v_cache) + prow * D, run * D, full);
+                            if constexpr (MODE == 2)
+                                bulk_g2s(sm + (is_k ? L::kKs : L::kVs) + slot * kBN * 4 + bi * run * 4,
+                                         (is_k ? a.k_scale : a.v_scale) + prow, run * 4, full);
+                        }
+                    }
+                    return true;
+                };
+                ok = stage(true);
+                if (!ok) break;
+                issued_k = t + 1;
+                ok = stage(false);
+                if (!ok) break;
+                issued_v = t + 1;
             }
-            issued_k = j + 1;
-            if (!stage(false)) {
-                ok = false;
-                break;
-            }
-            issued_v = j + 1;
+            g += u.tiles;
         }
         __syncwarp();
-        if (!ok && lane == 0) {
-            set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
-            // copies still in flight: wait for them before the CTA exits
-            for (int j = max(0, issued_k - kNK); j < issued_k; ++j) mbar_wait(&bars->k_full[j % kNK], (j / kNK) & 1);
-            for (int j = max(0, issued_v - kNV); j < issued_v; ++j)
+        if (lane == 0) {
+            if (!ok) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
+            // copies still in flight (only after a timeout): wait for them before the CTA exits
+            for (uint32_t j = issued_k > kNK ? issued_k - kNK : 0; j < issued_k; ++j)
+                mbar_wait(&bars->k_full[j % kNK], (j / kNK) & 1);
+            for (uint32_t j = issued_v > kNV ? issued_v - kNV : 0; j < issued_v; ++j)
                 mbar_wait(kFp8 ? &bars->raw_full[j % kNV] : &bars->v_full[j % kNV], (j / kNV) & 1);
         }
         __syncwarp();
@@ -757,9 +888,11 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
             constexpr uint32_t kIdescS = kFp8 ? idesc_f16(kRows, kBN, false) : idesc_bf16(kRows, kBN, false);
             constexpr uint32_t kIdescPV = MODE == 1 ? idesc_f16(kRows, D, true) : idesc_bf16(kRows, D, true);
             const uint32_t sq = base + L::kQ;
-            auto issue_s = [&](int j) {
-                const uint32_t sk = base + L::kK + (j % kNK) * L::kKSlot;
-                const uint32_t ts = tmem + (j & 1) * kBN;
+            auto issue_s = [&](uint32_t t) -> bool {
+                if (!mbar_wait(&bars->k_full[t % kNK], (t / kNK) & 1)) return false;
+                tc_fence_after();
+                const uint32_t sk = base + L::kK + (t % kNK) * L::kKSlot;
+                const uint32_t ts = tmem + (t & 1) * kBN;
                 if constexpr (kFp8) {  // E4M3: format code 0 for A and B, 32 elements per step; hi, then lo
 #pragma unroll
                     for (int kk = 0; kk < 2 * (D / 32); ++kk) {
@@ -776,31 +909,32 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                                  kk > 0 ? 1u : 0u);
                     }
                 }
-                mma_commit(&bars->k_empty[j % kNK]);
-                mma_commit(&bars->s_full[j & 1]);
+                mma_commit(&bars->k_empty[t % kNK]);
+                mma_commit(&bars->s_full[t & 1]);
+                return true;
             };
-            bool ok = mbar_wait(&bars->q_full, 0) && mbar_wait(&bars->k_full[0], 0);
-            tc_fence_after();
-            if (ok) issue_s(0);
-            for (int j = 0; ok && j < u.tiles; ++j) {
-                if (j + 1 < u.tiles) {  // its S buffer was P of tile j - 1, which P V(j - 1) read before
-                    ok = mbar_wait(&bars->k_full[(j + 1) % kNK], ((j + 1) / kNK) & 1);
+            bool ok = true;
+            for (int unit = 0; ok && walk.next(a, log2_g, u); ++unit) {
+                ok = mbar_wait(&bars->q_full, unit & 1) && issue_s(g);
+                for (int j = 0; ok && j < u.tiles; ++j) {
+                    const uint32_t t = g + j;
+                    // the next tile's S buffer was P of tile j - 1, which P V(j - 1) read before
+                    if (j + 1 < u.tiles) ok = issue_s(t + 1);
+                    ok = ok && mbar_wait(&bars->p_full[t & 1], (t >> 1) & 1) &&
+                         mbar_wait(&bars->v_full[t % kNV], (t / kNV) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_s(j + 1);
-                }
-                ok = mbar_wait(&bars->p_full[j & 1], (j >> 1) & 1) && mbar_wait(&bars->v_full[j % kNV], (j / kNV) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sv = base + L::kV + (j % kNV) * L::kVSlot;
+                    const uint32_t sv = base + L::kV + (t % kNV) * L::kVSlot;
 #pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk)
-                    mma_bf16_ts(tmem + 128, tmem + (j & 1) * kBN + kk * 8,
-                                sw128_desc(sv + static_cast<uint32_t>(kk * 16 * 128), kBN * 128, 1024), kIdescPV,
-                                (j > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(&bars->v_empty[j % kNV]);
-                mma_commit(&bars->pv_done);
-                if (j + 1 == u.tiles) mma_commit(&bars->o_done);
+                    for (int kk = 0; kk < kBN / 16; ++kk)
+                        mma_bf16_ts(tmem + 128, tmem + (t & 1) * kBN + kk * 8,
+                                    sw128_desc(sv + static_cast<uint32_t>(kk * 16 * 128), kBN * 128, 1024), kIdescPV,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(&bars->v_empty[t % kNV]);
+                    mma_commit(&bars->pv_done);
+                    if (j + 1 == u.tiles) mma_commit(&bars->o_done);
+                }
+                g += u.tiles;
             }
             if (!ok) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
             // every MMA issued so far has finished before tensor memory is freed
@@ -814,44 +948,47 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
         constexpr int kCPR = D / 16;  // 16-code chunks per row
         const int ct = tid - 192;
         bool ok = true;
-        for (int j = 0; j < u.tiles; ++j) {
-            const int slot = j % kNV;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->raw_full[slot], (j / kNV) & 1)) ||
-                (j >= kNV && !__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[slot], (j / kNV - 1) & 1)))) {
-                ok = false;
-                break;
-            }
-            const int end = min(kBN, u.t1 - (u.t0 + j * kBN));  // rows past the end become zeros
-            const uint8_t *src = sm + L::kRaw + slot * L::kRawSlot;
-            const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + slot * kBN;
-            const uint32_t dst = base + L::kV + slot * L::kVSlot;
-#pragma unroll
-            for (int i0 = 0; i0 < kBN * kCPR; i0 += kCT) {
-                const int i = i0 + ct;
-                const int rr = i / kCPR, cc = i % kCPR;
-                const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
-                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                if (rr < end) {
-                    if constexpr (MODE == 2) {
-                        const float s = vs[rr];
-                        lo = e4m3x8_scaled_bf16x8(make_uint2(w.x, w.y), s);
-                        hi = e4m3x8_scaled_bf16x8(make_uint2(w.z, w.w), s);
-                    } else {
-                        const uint2 h0 = e4m3x4_to_f16x4(w.x), h1 = e4m3x4_to_f16x4(w.y);
-                        const uint2 h2 = e4m3x4_to_f16x4(w.z), h3 = e4m3x4_to_f16x4(w.w);
-                        lo = make_uint4(h0.x, h0.y, h1.x, h1.y);
-                        hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
-                    }
+        while (ok && walk.next(a, log2_g, u)) {
+            for (int j = 0; j < u.tiles; ++j) {
+                const uint32_t t = g + j, slot = t % kNV;
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->raw_full[slot], (t / kNV) & 1)) ||
+                    (t >= kNV && !__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[slot], (t / kNV - 1) & 1)))) {
+                    ok = false;
+                    break;
                 }
-                st_shared16(dst + swz(kBN, rr, 2 * cc), lo);
-                st_shared16(dst + swz(kBN, rr, 2 * cc + 1), hi);
+                const int end = min(kBN, u.t1 - (u.t0 + j * kBN));  // rows past the end become zeros
+                const uint8_t *src = sm + L::kRaw + slot * L::kRawSlot;
+                const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + slot * kBN;
+                const uint32_t dst = base + L::kV + slot * L::kVSlot;
+#pragma unroll
+                for (int i0 = 0; i0 < kBN * kCPR; i0 += kCT) {
+                    const int i = i0 + ct;
+                    const int rr = i / kCPR, cc = i % kCPR;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
+                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                    if (rr < end) {
+                        if constexpr (MODE == 2) {
+                            const float s = vs[rr];
+                            lo = e4m3x8_scaled_bf16x8(make_uint2(w.x, w.y), s);
+                            hi = e4m3x8_scaled_bf16x8(make_uint2(w.z, w.w), s);
+                        } else {
+                            const uint2 h0 = e4m3x4_to_f16x4(w.x), h1 = e4m3x4_to_f16x4(w.y);
+                            const uint2 h2 = e4m3x4_to_f16x4(w.z), h3 = e4m3x4_to_f16x4(w.w);
+                            lo = make_uint4(h0.x, h0.y, h1.x, h1.y);
+                            hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
+                        }
+                    }
+                    st_shared16(dst + swz(kBN, rr, 2 * cc), lo);
+                    st_shared16(dst + swz(kBN, rr, 2 * cc + 1), hi);
+                }
+                fence_proxy_async_smem();  // P V reads the tile through the async proxy
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars->v_full[slot]);
+                    mbar_arrive(&bars->raw_empty[slot]);
+                }
             }
-            fence_proxy_async_smem();  // P V reads the tile through the async proxy
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars->v_full[slot]);
-                mbar_arrive(&bars->raw_empty[slot]);
-            }
+            g += u.tiles;
         }
         if (!ok && lane == 0) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
         __syncwarp();
@@ -865,55 +1002,67 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
     }
 }
 
-// Join of a sequence's partitions: one warp per (draft, query head).
-constexpr int kJoinWarps = 4;
+// Join of the cut units: block i looks at the border between the shares i and
+// i + 1; if it cuts a unit, the block makes its part of that unit's results
+// (the borders inside one unit divide its results among them).
+constexpr int kJoinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(TreeArgs a, int blocks_per_seq) {
-    constexpr int E = D / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.x / blocks_per_seq;
-    const int item = (blockIdx.x % blocks_per_seq) * kJoinWarps + warp;  // draft * num_q_heads + head
-    const int q0 = __ldg(a.cu_q_lens + s), q1 = __ldg(a.cu_q_lens + s + 1), ctx = __ldg(a.context_lens + s);
-    if (q0 < 0 || q1 < q0 || q1 > a.total_q) return;
-    const int c = q1 - q0;
-    if (c > a.max_q_len || ctx < c || ctx > a.max_context_len) return;  // the attention kernel's zeros
-    if (item >= c * a.num_q_heads) return;
-    const int parts = (ctx + a.partition_tokens - 1) / a.partition_tokens;
-    if (parts <= 1) return;
-    const long long prow = static_cast<long long>(s) * a.max_q_len * a.num_q_heads + item;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + prow * a.num_partitions;
-    const float *po = a.part_o + prow * a.num_partitions * D + lane * E;
-    float top = -INFINITY;
-    bool bad = false;
-    for (int i = lane; i < parts; i += 32) {
-        const float2 x = ml[i];
-        top = fmaxf(top, x.x);
-        bad |= x.y < 0.0f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    bad = __any_sync(0xffffffffu, bad);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    float sum = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-        const float2 x = ml[i];
-        if (x.y == 0.0f) continue;
-        const float w = fast_exp2(x.x - ref) * x.y;
-        sum += w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, po[static_cast<long long>(i) * D + e], acc[e]);
-    }
-    const float inv = (bad || sum == 0.0f) ? 0.0f : 1.0f / sum;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (static_cast<long long>(q0) * a.num_q_heads + item) * D +
-                         lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        const uint32_t w = bad ? 0u : pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-        *reinterpret_cast<uint32_t *>(out + e) = w;
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int log2_g) {
+    __shared__ long long scratch[9];
+    const int tid = threadIdx.x, G = 1 << log2_g;
+    const Shares sh = count_shares<kJoinThreads>(a, log2_g, scratch);
+    const int border = blockIdx.x + 1;
+    if (border >= sh.shares) return;
+    const long long x = sh.begin(border);
+    long long p;
+    const int s = find_seq<kJoinThreads>(a, log2_g, x, scratch, p);
+    const Seq q = load_seq(a, s, log2_g);
+    const int k = static_cast<int>((x - p) / (q.tiles + kUnitCost));
+    p += static_cast<long long>(k) * (q.tiles + kUnitCost);
+    const int cut = tiles_before(x, p, q.tiles);
+    if (cut == 0 || cut == q.tiles) return;
+    int first = border - 1, end = border + 1;  // the shares that hold a piece
+    while (tiles_before(sh.begin(first), p, q.tiles) > 0) --first;
+    while (end < sh.shares && tiles_before(sh.begin(end), p, q.tiles) < q.tiles) ++end;
+    const int pieces = end - first, part = border - 1 - first, parts = pieces - 1;
+    const int kh = k / q.row_tiles, row0 = (k % q.row_tiles) * kRows;
+    const int rows = min(kRows, (q.c << log2_g) - row0);
+    const long long slot_rows = min(static_cast<long long>(kRows), static_cast<long long>(a.max_q_len) << log2_g);
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+    // a unit's first piece is in its share's second slot, the others in the first ones
+    auto slot = [&](int i) { return i == 0 ? 2LL * first + 1 : 2LL * (first + i); };
+    for (int i = part * kJoinThreads + tid; i < rows * (D / 4); i += parts * kJoinThreads) {
+        const int r = i / (D / 4), col = (i % (D / 4)) * 4;
+        float top = -INFINITY;
+        bool bad = false;
+        for (int n = 0; n < pieces; ++n) {
+            const float2 y = __ldg(ml + slot(n) * slot_rows + r);
+            top = fmaxf(top, y.x);
+            bad |= y.y < 0.0f;
+        }
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        float4 acc = make_float4(0, 0, 0, 0);
+        for (int n = 0; n < pieces; ++n) {
+            const float2 y = __ldg(ml + slot(n) * slot_rows + r);
+            if (y.y == 0.0f) continue;  // a piece that the row saw nothing of
+            const float w = fast_exp2(y.x - ref) * y.y;
+            const float4 o = __ldg(reinterpret_cast<const float4 *>(a.part_o + (slot(n) * slot_rows + r) * D + col));
+            sum += w;
+            acc.x = fmaf(w, o.x, acc.x);
+            acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z);
+            acc.w = fmaf(w, o.w, acc.w);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int row = row0 + r;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                             (static_cast<long long>(q.q0 + (row >> log2_g)) * a.num_q_heads + kh * G + (row & (G - 1))) * D +
+                             col;
+        *reinterpret_cast<uint2 *>(dst) = bad ? make_uint2(0, 0)
+                                              : make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
+                                                           pack_bf16(acc.z * inv, acc.w * inv));
     }
 }
 
@@ -944,9 +1093,6 @@ cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
     while ((1 << log2_g) < g) ++log2_g;
     // row coordinates of the tensor maps are int32
     if (a.num_blocks * a.num_kv_heads * a.block_size > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const long long row_tiles = (static_cast<long long>(a.max_q_len) * g + kRows - 1) / kRows;
-    const long long units = row_tiles * a.num_kv_heads * a.num_seqs;
-    if (row_tiles > 0x7fffffffLL || units > 0x7fffffffLL / a.num_partitions) return cudaErrorInvalidConfiguration;
     CUtensorMap mk, mv;
     memset(&mv, 0, sizeof(mv));
     if (!make_map(&mk, a.k_cache, a) || (MODE == 0 && !make_map(&mv, a.v_cache, a))) return cudaErrorInvalidValue;
@@ -961,23 +1107,20 @@ cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    kern<<<static_cast<unsigned>(units * a.num_partitions), tree_threads<MODE>(), L::kAlloc, stream>>>(
-        a, log2_bs, log2_g, static_cast<int>(row_tiles), mk, mv);
+    kern<<<a.max_shares, tree_threads<MODE>(), L::kAlloc, stream>>>(a, log2_bs, log2_g, mk, mv);
     e = cudaGetLastError();
-    if (e != cudaSuccess || a.partition_tokens == 0) return e;
-    const long long per_seq = (static_cast<long long>(a.max_q_len) * a.num_q_heads + kJoinWarps - 1) / kJoinWarps;
-    const long long blocks = per_seq * a.num_seqs;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    tree_join_kernel<D><<<static_cast<unsigned>(blocks), 32 * kJoinWarps, 0, stream>>>(a, static_cast<int>(per_seq));
+    if (e != cudaSuccess || a.max_shares == 1) return e;
+    tree_join_kernel<D><<<a.max_shares - 1, kJoinThreads, 0, stream>>>(a, log2_g);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int tree_tile_tokens() { return kBN; }
-int tree_row_tiles(int max_q_len, int group) {
-    return static_cast<int>((static_cast<long long>(max_q_len) * group + kRows - 1) / kRows);
+int tree_slot_rows(int max_q_len, int group) {
+    const long long rows = static_cast<long long>(max_q_len) * group;
+    return rows < kRows ? static_cast<int>(rows) : kRows;
 }
+int tree_min_share() { return kMinShare; }
 
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
     if (a.head_dim == 128)

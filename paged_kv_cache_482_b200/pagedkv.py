@@ -66,6 +66,10 @@ class _Plan(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class _TreePlan(ctypes.Structure):
+    _fields_ = [("shares", ctypes.c_int), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -120,7 +124,7 @@ def load_library(path: str):
     L.pkv_store_kvcache_norm_rope.argtypes = ([vp, i64] * 4 + [vp, vp, f32] + [vp] * 5 + [i32] * 7
                                               + [i64, i32, vp, vp, vp, vp])
     L.pkv_store_kvcache_norm_rope.restype = i32
-    L.pkv_plan_tree.argtypes = [i32] * 9 + [c.POINTER(_Plan)]
+    L.pkv_plan_tree.argtypes = [i32] * 9 + [c.POINTER(_TreePlan)]
     L.pkv_plan_tree.restype = i32
     L.pkv_paged_attention_tree.argtypes = ([vp] * 4 + [i32, vp, vp, vp] + [i32] * 7 + [i64, f32, i32, vp, vp, i32, i32,
                                                                                       i32, vp, sz, vp, vp, vp])
@@ -564,26 +568,26 @@ def tree_mask(parents, words=None):
 
 
 def plan_tree(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_context_len,
-              cache_dtype=PKV_CACHE_BF16, partition_request=0) -> dict:
-    """The split plan and workspace size of a ``paged_attention_tree`` call of these sizes."""
-    plan = _Plan()
+              cache_dtype=PKV_CACHE_BF16, shares=0) -> dict:
+    """The shares and workspace size of a ``paged_attention_tree`` call of these sizes."""
+    plan = _TreePlan()
     st = lib().pkv_plan_tree(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_context_len,
-                             int(cache_dtype), partition_request, ctypes.byref(plan))
+                             int(cache_dtype), shares, ctypes.byref(plan))
     _check(st, "pkv_plan_tree")
-    return dict(partition_tokens=plan.partition_tokens, max_partitions=plan.max_partitions,
-                workspace_bytes=plan.workspace_bytes)
+    return dict(shares=plan.shares, workspace_bytes=plan.workspace_bytes)
 
 
 def paged_attention_tree(q, k_cache, v_cache, block_tables, cu_q_lens, context_lens, tree_mask, scale, max_q_len,
-                         out=None, k_scale=None, v_scale=None, max_context_len=None, partition_request=0,
-                         workspace=None, dev_err=None, stream=None):
+                         out=None, k_scale=None, v_scale=None, max_context_len=None, shares=0, workspace=None,
+                         dev_err=None, stream=None):
     """Attention of drafted trees over the paged cache: the drafts of sequence
     i (rows ``cu_q_lens[i]`` .. ``cu_q_lens[i+1] - 1`` of ``q``, ``[total_q,
     nq, d]`` bf16) are the last of its ``context_lens[i]`` cached tokens; a row
     attends to every token before them and to the drafts whose bits are set in
     its row of ``tree_mask`` (``[total_q, words]`` int32, see ``tree_mask()``).
     A row that sees nothing is zeros. ``max_q_len`` and ``max_context_len``
-    (default: the block table's capacity) are host-known bounds. A workspace is
+    (default: the block table's capacity) are host-known bounds; ``shares`` is
+    the number of thread blocks (0: chosen). A workspace is
     allocated when the plan (``plan_tree``) needs one and none is given; calls
     that may overlap need workspaces of their own."""
     if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
@@ -609,14 +613,14 @@ def paged_attention_tree(q, k_cache, v_cache, block_tables, cu_q_lens, context_l
     if out is None:
         out = _empty(q.shape, torch.bfloat16, dev, stream)
     if workspace is None:
-        need = plan_tree(S, nq, nkv, d, bs, max_q_len, max_context_len, dt, partition_request)["workspace_bytes"]
+        need = plan_tree(S, nq, nkv, d, bs, max_q_len, max_context_len, dt, shares)["workspace_bytes"]
         if need:
             workspace = _empty(need, torch.uint8, dev, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _run(lib().pkv_paged_attention_tree, "pkv_paged_attention_tree", dev, stream, _addr(q), _addr(k_cache),
          _addr(v_cache), _addr(block_tables), maxb, _addr(cu_q_lens), _addr(context_lens), _addr(tree_mask), words, S,
          T, nq, nkv, d, bs, nblk, scale, dt, _addr(k_scale), _addr(v_scale), max_q_len, max_context_len,
-         partition_request, _addr(workspace), ws_bytes, _addr(out), _addr(dev_err))
+         shares, _addr(workspace), ws_bytes, _addr(out), _addr(dev_err))
     return out
 
 

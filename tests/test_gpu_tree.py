@@ -110,12 +110,14 @@ def test_wide_trees(G, cache):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
-@pytest.mark.parametrize("part", [-1, 0, 1, 200, 1000])
-def test_partitions_agree(cache, part):
-    c = make([4, 9, 1, 20], [2500, 70, 1, 1111], 8, 2, 128, 16, cache, seed=11)
-    p = K.plan_tree(4, 8, 2, 128, 16, 20, 2512, cache_dtype=K.cache_dtype(c["kp"], c["ks"]), partition_request=part)
-    ws = torch.full((max(256, p["workspace_bytes"]),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN
-    check(c, partition_request=part, workspace=ws)
+@pytest.mark.parametrize("shares", [0, 1, 2, 3, 10, 37, 300])
+def test_any_cut_of_the_work(cache, shares):
+    """One block for everything, a few, and more blocks than tiles: units whole,
+    cut once, cut many times, and joined from a workspace of NaN."""
+    c = make([4, 9, 1, 20, 50], [2500, 70, 1, 1111, 180], 8, 2, 128, 16, cache, seed=11)
+    p = K.plan_tree(5, 8, 2, 128, 16, 50, 2512, cache_dtype=K.cache_dtype(c["kp"], c["ks"]), shares=shares)
+    ws = torch.full((max(256, p["workspace_bytes"]),), 0xFF, dtype=torch.uint8, device="cuda")
+    check(c, shares=shares, workspace=ws)
 
 
 def test_rows_without_keys_are_zeros_and_others_are_not():

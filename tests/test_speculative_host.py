@@ -61,7 +61,7 @@ def test_tree_abi_refusals(K):
     L = K.lib()
     ok = dict(q=0x10000, kc=0x20000, vc=0x30000, bt=0x40000, maxb=8, cu=0x50000, cl=0x60000, mask=0x61000, words=2,
               S=4, T=100, nq=32, nkv=8, d=128, bs=256, nblk=100, scale=0.088, dt=0, ks=None, vs=None, mq=64,
-              mc=2048, part=-1, ws=None, wsb=0, out=0x70000)
+              mc=2048, part=1, ws=None, wsb=0, out=0x70000)
 
     def call(**kw):
         a = dict(ok)
@@ -86,7 +86,10 @@ def test_tree_abi_refusals(K):
     assert call(words=0) == K.PKV_ERR_INVALID_ARG
     assert call(mc=2049) == K.PKV_ERR_INVALID_ARG  # beyond the table
     assert call(mc=0) == K.PKV_ERR_INVALID_ARG
-    assert call(part=-2) == K.PKV_ERR_INVALID_ARG
+    assert call(part=-1) == K.PKV_ERR_INVALID_ARG and call(part=4097) == K.PKV_ERR_INVALID_ARG
+    assert call(part=0) == K.PKV_ERR_WORKSPACE and call(part=2, ws=0x80000, wsb=64) == K.PKV_ERR_WORKSPACE
+    assert call(part=2, ws=0x80010, wsb=1 << 30) == K.PKV_ERR_INVALID_ARG  # not 256-byte aligned
+    assert call(S=0, part=2, ws=0x80000, wsb=1 << 30) == K.PKV_OK
     assert call(nblk=2**31) == K.PKV_ERR_INVALID_ARG
     assert call(S=-1) == K.PKV_ERR_INVALID_ARG and call(T=-1) == K.PKV_ERR_INVALID_ARG
     assert call(S=0) == K.PKV_OK and call(T=0) == K.PKV_OK
@@ -221,21 +224,22 @@ def test_tree_mask_helper(K):
 
 
 def test_tree_plan(K):
-    """The workspace holds every partition of the longest context."""
+    """The workspace holds two partials of up to 128 rows for every share."""
     for args in ((1, 32, 8, 128, 256, 8, 512), (64, 32, 8, 128, 16, 32, 32768), (1, 4, 4, 64, 8, 1, 1),
                  (3, 8, 1, 64, 1024, 300, 40000)):
+        rows = min(128, args[5] * args[1] // args[2])
         for dt in (K.PKV_CACHE_BF16, K.PKV_CACHE_FP8_E4M3, K.PKV_CACHE_FP8_E4M3_TOKEN):
-            p = K.plan_tree(*args, cache_dtype=dt)
-            if p["partition_tokens"]:
-                assert p["partition_tokens"] * p["max_partitions"] >= args[6] > \
-                    p["partition_tokens"] * (p["max_partitions"] - 1)
-                assert p["workspace_bytes"] >= args[0] * args[5] * args[1] * p["max_partitions"] * (args[3] + 2) * 4
-            else:
-                assert p["workspace_bytes"] == 0 and p["max_partitions"] == 1
-            p = K.plan_tree(*args, cache_dtype=dt, partition_request=-1)
-            assert p["partition_tokens"] == 0 and p["workspace_bytes"] == 0
+            for shares in (0, 1, 2, 77, 4096):
+                p = K.plan_tree(*args, cache_dtype=dt, shares=shares)
+                n = p["shares"]
+                assert n == shares if shares else n >= 2
+                least = 2 * n * rows * (args[3] + 2) * 4 if n > 1 else 0
+                assert least <= p["workspace_bytes"] <= least + 512
     for bad in ((1, 32, 8, 96, 256, 8, 512), (1, 24, 8, 128, 256, 8, 512), (1, 32, 8, 128, 100, 8, 512),
-                (1, 32, 8, 128, 256, 0, 512), (1, 32, 8, 128, 256, 8, 0), (-1, 32, 8, 128, 256, 8, 512)):
+                (1, 32, 8, 128, 256, 0, 512), (1, 32, 8, 128, 256, 8, 0), (-1, 32, 8, 128, 256, 8, 512),
+                (1, 32, 8, 128, 256, 8, 512, 0, -1), (1, 32, 8, 128, 256, 8, 512, 0, 4097),
+                (1, 32, 8, 128, 256, 8, 512, 3)):
         with pytest.raises(K.PagedKVError):
             K.plan_tree(*bad)
-    assert K.lib().pkv_plan_tree(1, 32, 8, 128, 256, 8, 512, 0, 0, ctypes.POINTER(K._Plan)()) == K.PKV_ERR_INVALID_ARG
+    assert K.lib().pkv_plan_tree(1, 32, 8, 128, 256, 8, 512, 0, 0, ctypes.POINTER(K._TreePlan)()) == \
+        K.PKV_ERR_INVALID_ARG

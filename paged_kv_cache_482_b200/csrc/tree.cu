@@ -145,24 +145,31 @@ __device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t
         : "memory");
 }
 
-// N consecutive columns of this thread's tensor-memory lane (N 16, 32 or 64).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
+// 16 consecutive columns of this thread's tensor-memory lane. The load is
+// asynchronous: the registers hold the columns after tmem_wait16.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        "%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <int N>
-__device__ __forceinline__ void tmem_ldn(uint32_t taddr, float (&v)[N]) {
-    if constexpr (N == 16) tmem_ld16(taddr, v);
-    else if constexpr (N == 32) tmem_ld32(taddr, v);
-    else tmem_ld64(taddr, v);
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+// 8 columns, waited for.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
 }
 
 // 8 columns into this thread's lane, not waited for.
@@ -390,10 +397,16 @@ __device__ __forceinline__ bool mend_v(uint32_t sv, int first, int end, bool zer
     return found;
 }
 
-// Softmax of this warp's rows over the unit's tiles: COLS keys of every tile (64
-// / copies). g0: tiles of the units before. Leaves the reference maximum and the
-// sum of the row (copy).
-template <int D, int MODE, int COLS>
+// A weight pair, rounded to the operand type, and what it adds to the normaliser.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_p(float p0, float p1) { return F16 ? pack_f16(p0, p1) : pack_bf16(p0, p1); }
+
+// Softmax of this warp's rows over the unit's tiles: 64 / copies keys of every
+// tile, 16 at a time in a loop (written out for 64 keys, in one variant per
+// number of copies, the code outgrew the instruction cache: a CTA's first tile
+// took 8000 cycles). g0: tiles of the units before. Leaves the reference maximum
+// and the sum of the row (copy).
+template <int D, int MODE>
 __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, TreeBars *bars, uint8_t *sm,
                                               uint32_t base, uint32_t tmem, float sl2, bool live, int draft,
                                               uint32_t g0, int unit, float &m_out, float &l_out) {
@@ -402,111 +415,108 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const bool idle = !__any_sync(0xffffffffu, live);  // no row in this warp: its weights are never read
-    const int copy = COLS == 64 ? 0 : (warp * 32) / u.per_copy;
-    const int col0 = copy * COLS;
+    const int groups = 4 / u.copies;                   // of 16 keys
+    const int group0 = (warp * 32) / u.per_copy * groups;
     const uint32_t *mask = a.mask + static_cast<long long>(u.q0 + draft) * a.mask_words;
+    const uint32_t to = tmem + 128 + lane_base;
     float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
     for (int j = 0; j < u.tiles; ++j) {
         const uint32_t g = g0 + j;
         const int kv0 = u.t0 + j * kBN;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[g & 1], (g >> 1) & 1))) return false;
         tc_fence_after();
         const bool special = kv0 + kBN > u.base;  // holds drafts, or keys past the end
-        if (idle) {
-            if constexpr (MODE == 2) {
-                if (lane == 0) mbar_arrive(&bars->k_empty[g % kNK]);
-            }
-        } else {
+        if (!idle) {
             const uint32_t ts = tmem + (g & 1) * kBN + lane_base;
-            float x[COLS];
-            tmem_ldn<COLS>(ts + col0, x);
-            if constexpr (MODE == 2) {
-                const int slot = g % kNK;
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_full[slot], (g / kNK) & 1))) return false;
-                const float4 *ks = reinterpret_cast<const float4 *>(sm + L::kKs + slot * kBN * 4 + col0 * 4);
-#pragma unroll
-                for (int i = 0; i < COLS / 4; ++i) {
-                    const float4 k4 = ks[i];
-                    x[4 * i] *= k4.x * sl2;
-                    x[4 * i + 1] *= k4.y * sl2;
-                    x[4 * i + 2] *= k4.z * sl2;
-                    x[4 * i + 3] *= k4.w * sl2;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < COLS; ++i) x[i] *= sl2;
-            }
-            if (special) {
-#pragma unroll
-                for (int h = 0; h < (COLS + 31) / 32; ++h) {
-                    const uint32_t vis = live ? visible32(mask, u.c, kv0 + col0 + 32 * h, u.base) : 0u;
-#pragma unroll
-                    for (int i = 0; i < (COLS < 32 ? COLS : 32); ++i)
-                        if (!((vis >> i) & 1u)) x[32 * h + i] = -INFINITY;
-                }
-            }
-            float m8[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m8[k] = x[k];
-#pragma unroll
-            for (int i = 8; i < COLS; ++i) m8[i & 7] = fmaxf(m8[i & 7], x[i]);
-            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-            float alpha = 1.0f;
-            bool rescale = false;
-            if (j == 0) {
-                m = mx;
-            } else {
-                const bool grow = mx > m + 8.0f;
-                rescale = __any_sync(0xffffffffu, grow);
-                if (grow) {
-                    alpha = fast_exp2(m - mx);
-                    m = mx;
-                    l *= alpha;
-                }
-            }
-            const float ref = m == -INFINITY ? 0.0f : m;  // nothing seen yet: weights exp2(-inf) = 0
+            uint32_t next[16];
+            tmem_ld16(ts + 16 * group0, next);
+            if (MODE == 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->k_full[g % kNK], (g / kNK) & 1))) return false;
+            const float *ks = reinterpret_cast<const float *>(sm + L::kKs) + (g % kNK) * kBN;
             float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (int h = group0; h < group0 + groups; ++h) {
+                float x[16];
+                tmem_wait16(next);
 #pragma unroll
-            for (int h = 0; h < COLS / 16; ++h) {
+                for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(next[i]) * sl2;
+                if (h + 1 < group0 + groups) tmem_ld16(ts + 16 * (h + 1), next);
+                if constexpr (MODE == 2) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + 16 * h + i);
+                        x[i] *= k4.x;
+                        x[i + 1] *= k4.y;
+                        x[i + 2] *= k4.z;
+                        x[i + 3] *= k4.w;
+                    }
+                }
+                if (special) {
+                    const uint32_t vis = live ? visible32(mask, u.c, kv0 + 16 * h, u.base) : 0u;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!((vis >> i) & 1u)) x[i] = -INFINITY;
+                }
+                float m4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(x[k], x[k + 4]), fmaxf(x[k + 8], x[k + 12]));
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const bool grow = mx > m + 8.0f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    // a new reference: what was formed with the old one is scaled
+                    const float alpha = grow ? fast_exp2(m - mx) : 1.0f;  // 0 from m = -inf
+                    if (grow) {
+                        m = mx;
+                        l *= alpha;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) l4[k] *= alpha;
+                    }
+#pragma unroll 1
+                    for (int e = group0; e < h; ++e) {  // this tile's weights
+                        uint32_t w[8];
+                        tmem_ld8(ts + 8 * e, w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const __half2 f = *reinterpret_cast<const __half2 *>(&w[i]);
+                            w[i] = pack_p<kF16>((kF16 ? __low2float(f) : bf16lo(w[i])) * alpha,
+                                                (kF16 ? __high2float(f) : bf16hi(w[i])) * alpha);
+                        }
+                        tmem_st8(ts + 8 * e, w);
+                    }
+                    if (j > 0) {  // S(j) done implies P V(j - 2) done: the next phase is P V(j - 1)
+                        if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (g - 1) & 1))) return false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int ch = 0; ch < D; ch += 8) {
+                            uint32_t w[8];
+                            tmem_ld8(to + ch, w);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+                            tmem_st8(to + ch, w);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : m;  // nothing seen yet: weights exp2(-inf) = 0
                 uint32_t w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float p0 = fast_exp2(x[16 * h + 2 * i] - ref), p1 = fast_exp2(x[16 * h + 2 * i + 1] - ref);
-                    if constexpr (kF16) {
-                        w[i] = pack_f16(p0, p1);
-                        l4[i & 3] = fma_f16x2_acc(w[i], 0x3C003C00u, l4[i & 3]);
-                    } else {
-                        w[i] = pack_bf16(p0, p1);
-                        l4[i & 3] = fma_bf16x2_acc(w[i], 0x3F803F80u, l4[i & 3]);
-                    }
+                    w[i] = pack_p<kF16>(fast_exp2(x[2 * i] - ref), fast_exp2(x[2 * i + 1] - ref));
+                    l4[i & 3] = kF16 ? fma_f16x2_acc(w[i], 0x3C003C00u, l4[i & 3])
+                                     : fma_bf16x2_acc(w[i], 0x3F803F80u, l4[i & 3]);
                 }
-                tmem_st8(ts + col0 / 2 + 8 * h, w);
-            }
-            if constexpr (COLS < 64) {  // the other copies' keys
-                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-                for (int h = COLS / 16; h < 4; ++h) tmem_st8(ts + ((col0 / 2 + 8 * h) & 31), zero);
+                tmem_st8(ts + 8 * h, w);
             }
             l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-            if constexpr (MODE == 2) {
-                // here, behind instructions that used every lane's scales: released right
-                // after the loads, the slot was refilled under lanes still reading it
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->k_empty[g % kNK]);
+            if (groups < 4) {  // the other copies' keys
+                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                for (int h = groups; h < 4; ++h) tmem_st8(ts + ((8 * (group0 + h)) & 31), zero);
             }
-            if (rescale) {  // S(j) done implies P V(j - 2) done: the next phase is P V(j - 1)
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (g - 1) & 1))) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    float v[32];
-                    tmem_ld32(tmem + 128 + lane_base + ch * 32, v);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= alpha;
-                    tmem_st32_async(tmem + 128 + lane_base + ch * 32, v);
-                }
-            }
+        }
+        if constexpr (MODE == 2) {
+            // here, behind instructions that used every lane's scales: released right
+            // after the loads, the slot was refilled under lanes still reading it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->k_empty[g % kNK]);
         }
         if (special) {
             const int slot = g % kNV;
@@ -595,12 +605,17 @@ __device__ __forceinline__ void write_unit(const TreeArgs &a, const Unit &u, Tre
     const uint32_t tmem_o = tmem + 128 + (static_cast<uint32_t>((tid >> 5) * 32) << 16);
 #pragma unroll 1
     for (int ch = 0; ch < D / kCols; ++ch) {
-        float v[kCols];
-        tmem_ldn<kCols>(tmem_o + ch * kCols, v);
 #pragma unroll
-        for (int i = 0; i < kCols; i += 4)
-            *reinterpret_cast<float4 *>(o + tid * kStride + i) =
-                drop ? make_float4(0, 0, 0, 0) : make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
+        for (int i0 = 0; i0 < kCols; i0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(tmem_o + ch * kCols + i0, v);
+            tmem_wait16(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = drop ? 0u : __float_as_uint(__uint_as_float(v[i]) * f);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4 *>(o + tid * kStride + i0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
         named_sync(1, kSoftmaxWarps * 32);
         constexpr int kPer = kCols / 8;  // 8 columns a thread
         for (int i = tid; i < u.rows * kPer; i += kSoftmaxWarps * 32) {
@@ -739,14 +754,16 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
             } else {
                 const uint4 *qrow = reinterpret_cast<const uint4 *>(
                     qp + (static_cast<long long>(u.q0 + draft) * a.num_q_heads + head) * D);
-                uint4 qv[kChunks];
                 float amax = 0.0f;
+                if (live) {
+#pragma unroll 8
+                    for (int c16 = 0; c16 < kChunks; ++c16) {
+                        const uint4 v4 = __ldg(qrow + c16);
+                        const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-                for (int c16 = 0; c16 < kChunks; ++c16) {
-                    qv[c16] = live ? __ldg(qrow + c16) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {qv[c16].x, qv[c16].y, qv[c16].z, qv[c16].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
+                        for (int k = 0; k < 4; ++k)
+                            amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
+                    }
                 }
                 // amax < 2^e; times 2^kq it lies in [2^7, 2^8). kq is capped at 60
                 // so that 2^-kq times the softmax scale stays normal: rows that
@@ -757,15 +774,15 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                 sl2 *= __int_as_float((127 - kq) << 23);
                 if (MODE == 1) sl2 *= __ldg(a.k_scale + u.kh);
                 if (!(amax <= 3.4e38f)) sl2 = __int_as_float(0x7FC00000);  // an infinite query: E4M3 has none
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {  // 16 elements: one chunk of hi and of lo
+                    const uint4 v0 = live ? __ldg(qrow + 2 * c) : make_uint4(0, 0, 0, 0);
+                    const uint4 v1 = live ? __ldg(qrow + 2 * c + 1) : make_uint4(0, 0, 0, 0);
+                    const uint32_t wv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const uint4 v4 = qv[2 * c + k / 4];
-                        const uint32_t wv[4] = {v4.x, v4.y, v4.z, v4.w};
-                        const uint32_t w = wv[k & 3];
-                        const float x = bf16lo(w) * qs, y = bf16hi(w) * qs;
+                        const float x = bf16lo(wv[k]) * qs, y = bf16hi(wv[k]) * qs;
                         const uint16_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
                         const float2 hf = e4m3x2_to_float2(h);
                         const uint16_t o =
@@ -791,13 +808,8 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                 if (id < 0 || id >= a.num_blocks) bars->bad[unit & 1] = 1;
             }
             float m = -INFINITY, l = 0.0f;
-            bool ok;
-            if (u.copies == 4)
-                ok = softmax_tiles<D, MODE, 16>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
-            else if (u.copies == 2)
-                ok = softmax_tiles<D, MODE, 32>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
-            else
-                ok = softmax_tiles<D, MODE, 64>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
+            const bool ok =
+                softmax_tiles<D, MODE>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
             if (!ok && lane == 0) {
                 set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
                 bars->failed = 1;
@@ -863,12 +875,12 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                     }
                     return true;
                 };
-                ok = stage(true);
+#pragma unroll 1
+                for (int which = 0; which < 2 && ok; ++which) {
+                    ok = stage(which == 0);
+                    if (ok) (which == 0 ? issued_k : issued_v) = t + 1;
+                }
                 if (!ok) break;
-                issued_k = t + 1;
-                ok = stage(false);
-                if (!ok) break;
-                issued_v = t + 1;
             }
             g += u.tiles;
         }
@@ -960,7 +972,7 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                 const uint8_t *src = sm + L::kRaw + slot * L::kRawSlot;
                 const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + slot * kBN;
                 const uint32_t dst = base + L::kV + slot * L::kVSlot;
-#pragma unroll
+#pragma unroll 2
                 for (int i0 = 0; i0 < kBN * kCPR; i0 += kCT) {
                     const int i = i0 + ct;
                     const int rr = i / kCPR, cc = i % kCPR;

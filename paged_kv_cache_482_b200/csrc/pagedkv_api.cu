@@ -498,10 +498,11 @@ int pkv_plan_tree(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                     max_context_len, cache_dtype);
     if (st != PKV_OK) return st;
     if (shares < 0 || shares > kMaxTreeShares) return PKV_ERR_INVALID_ARG;
-    plan->shares = shares > 0 ? shares : 2 * num_sms();
+    const int group = num_q_heads / num_kv_heads;
+    plan->shares = shares > 0 ? shares : pkv::tree_ctas_per_sm(max_q_len, group) * num_sms();
     plan->workspace_bytes = 0;
     if (plan->shares > 1) {
-        const size_t rows = (size_t)2 * plan->shares * pkv::tree_slot_rows(max_q_len, num_q_heads / num_kv_heads);
+        const size_t rows = (size_t)2 * plan->shares * pkv::tree_slot_rows(max_q_len, group);
         plan->workspace_bytes = round_up(rows * head_dim * sizeof(float), 256) + round_up(rows * 2 * sizeof(float), 256);
     }
     return PKV_OK;
@@ -556,10 +557,12 @@ int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_c
     a.max_context_len = max_context_len;
     a.max_shares = plan.shares;
     a.min_share = shares > 0 ? 1 : pkv::tree_min_share();
+    a.unit_rows = pkv::tree_unit_rows(max_q_len, num_q_heads / num_kv_heads);
+    a.slot_rows = pkv::tree_slot_rows(max_q_len, num_q_heads / num_kv_heads);
     a.part_o = nullptr;
     a.part_ml = nullptr;
     if (plan.workspace_bytes > 0) {
-        const size_t rows = (size_t)2 * plan.shares * pkv::tree_slot_rows(max_q_len, num_q_heads / num_kv_heads);
+        const size_t rows = (size_t)2 * plan.shares * a.slot_rows;
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                               round_up(rows * head_dim * sizeof(float), 256));

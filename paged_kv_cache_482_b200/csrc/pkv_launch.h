@@ -249,13 +249,17 @@ struct TreeArgs {
     int max_context_len;
     int max_shares;  // CTAs; shares of at least min_share tiles of work
     int min_share;
-    float *part_o;   // [2 max_shares][tree_slot_rows][head_dim]
-    float *part_ml;  // [2 max_shares][tree_slot_rows][2]
+    int unit_rows;  // rows (drafts x heads of a group) a CTA works on at a time
+    int slot_rows;  // rows of a workspace slot
+    float *part_o;   // [2 max_shares][slot_rows][head_dim]
+    float *part_ml;  // [2 max_shares][slot_rows][2]
     void *out;
     int *dev_err;
 };
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream);
+int tree_unit_rows(int max_q_len, int group);
 int tree_slot_rows(int max_q_len, int group);
+int tree_ctas_per_sm(int max_q_len, int group);
 int tree_min_share();
 
 bool prefill_supported(int head_dim, int group);

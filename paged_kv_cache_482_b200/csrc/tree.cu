@@ -13,25 +13,29 @@
 // byte, and the machine's ratio is some 230: below about that many rows the
 // cache's bytes bound the call, above it the tensor cores do.
 //
-// Work: a unit is (sequence, KV head, 128 rows), a row a (draft, head of the
-// group) pair. The units' key tiles, laid end to end, are cut into equal
-// shares, one per CTA, two CTAs per SM (one's joins and starts overlap the
-// other's stream): lengths need not be alike, no CTA idles, and a unit is cut
-// only where a share ends. A CTA computes its share from the lengths; the
-// partial results of cut units (at most two per CTA) go to the workspace and a
-// second kernel joins them. Warp roles:
-//   warps 0-3  softmax, one row per thread;
-//   warp 4     producer: copies 64-token K and V tiles into two rings, its lanes
-//              issuing one copy each (blocks smaller than the tile);
-//   warp 5     tensor-memory allocation and the MMA issue, S(0), then
-//              S(j + 1), P V(j), so that the tensor core forms the next scores
-//              while the softmax of tile j runs;
-//   warps 6-7  E4M3 only: widen the V codes of a tile into the ring P V reads.
-// Tensor memory (256 columns): two S buffers of 64 columns and O. P (16-bit
-// pairs) is written over the S it came from and is the A operand of P V.
+// Work: a unit is (sequence, KV head, 128 NT rows), a row a (draft, head of the
+// group) pair. NT = 1 for trees of at most 128 rows: two CTAs per SM, so that
+// one's unit changes overlap the other's stream. NT = 2 for wider ones: one CTA
+// per SM, every key tile multiplied with two row tiles, which halves the reads.
+// The units' key tiles, laid end to end, are cut into equal shares, one per CTA:
+// lengths need not be alike, no CTA idles, and a unit is cut only where a share
+// ends. A CTA computes its share from the lengths; the partial results of cut
+// units (at most two per CTA) go to the workspace and a second kernel joins
+// them. Warp roles:
+//   4 NT warps  softmax, one row per thread;
+//   1 warp      producer: copies 64-token K and V tiles into two rings, its lanes
+//               issuing one copy each (blocks smaller than the tile);
+//   1 warp      tensor-memory allocation and the MMA issue, S(0), then
+//               S(j + 1), P V(j), so that the tensor core forms the next scores
+//               while the softmax of tile j runs;
+//   2 NT warps  E4M3 only: widen the V codes of a tile into the ring P V reads.
+// Tensor memory (256 columns per row tile): two S buffers of 64 columns and O. P
+// (16-bit pairs) is written over the S it came from and is the A operand of P V.
+// Between units the next queries are loaded (and their first scores formed)
+// before the results are written.
 //
-// Few rows: with at most 32 (64) rows the tile holds 4 (2) copies of them, and
-// the warps of copy k handle only the k-th quarter (half) of the tile's keys,
+// Few rows: with at most a quarter (half) of the rows in use the unit holds 4 (2)
+// copies of them, and the warps of copy k handle the k-th quarter (half) of a tile's keys,
 // with weights of zero for the others: a copy is a split of the keys inside
 // the CTA, joined at the end of the unit. A thread then forms 16 (32)
 // exponentials per tile instead of 64.
@@ -67,58 +71,64 @@ using namespace tc;
 
 constexpr int kRows = 128;  // MMA M
 constexpr int kBN = 64;     // keys per tile
-constexpr int kSoftmaxWarps = 4;
-constexpr int kProducerWarp = 4;
-constexpr int kMmaWarp = 5;
-constexpr int kConvWarps = 2;  // E4M3: warps 6, 7
-constexpr int kNK = 2;         // ring depths (tiles)
-constexpr int kNV = 2;
-constexpr uint32_t kTmemCols = 256;  // S0 | S1 | O
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int MODE>
-constexpr int tree_threads() { return MODE == 0 ? 192 : 192 + 32 * kConvWarps; }
-
-template <int D, int MODE>
-struct TreeLayout {
+template <int D, int MODE, int NT>
+struct Tree {
     static constexpr bool kFp8 = MODE != 0;
-    static constexpr uint32_t kQ = 0;  // bf16 [D / 64][rows][128 B]; E4M3 hi, lo [rows][D B]
-    static constexpr uint32_t kQBytes = kRows * D * 2;
+    static constexpr bool kF16 = MODE == 1;  // type of P and V
+    static constexpr int kUnitRows = NT * kRows;
+    static constexpr int kSoftmaxWarps = 4 * NT;
+    static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+    static constexpr int kProducerWarp = kSoftmaxWarps;
+    static constexpr int kMmaWarp = kSoftmaxWarps + 1;
+    static constexpr int kFirstConvWarp = kSoftmaxWarps + 2;
+    static constexpr int kConvWarps = 2 * NT;
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + 2 + (kFp8 ? kConvWarps : 0));
+    static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
+    static constexpr uint32_t kTmemCols = 256 * NT;  // per row tile: S0 | S1 | O
+    // ring depths (tiles): keys, V as P V reads it, E4M3 V codes
+    static constexpr uint32_t kNK = NT == 1 ? 2 : 4;
+    static constexpr uint32_t kNV = NT == 1 ? 2 : (kFp8 ? 3 : 4);
+    static constexpr uint32_t kNR = NT == 1 ? 2 : 4;
+    static constexpr uint32_t kQTile = kRows * D * 2;  // bf16 [D / 64][rows][128 B]; E4M3 hi, lo [rows][D B]
     static constexpr uint32_t kKSlot = kBN * D * (kFp8 ? 1 : 2);
-    static constexpr uint32_t kVSlot = kBN * D * 2;   // what P V reads
-    static constexpr uint32_t kRawSlot = kFp8 ? kBN * D : 0;  // E4M3 V codes
-    static constexpr uint32_t kK = kQ + kQBytes;
+    static constexpr uint32_t kVSlot = kBN * D * 2;
+    static constexpr uint32_t kRSlot = kFp8 ? kBN * D : 0;
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kK = kQ + NT * kQTile;
     static constexpr uint32_t kV = kK + kNK * kKSlot;
-    static constexpr uint32_t kRaw = kV + kNV * kVSlot;
-    static constexpr uint32_t kKs = kRaw + kNV * kRawSlot;  // per-token scales [slot][kBN] fp32
+    static constexpr uint32_t kR = kV + kNV * kVSlot;
+    static constexpr uint32_t kKs = kR + kNR * kRSlot;  // per-token scales [slot][kBN] fp32
     static constexpr uint32_t kVs = kKs + (MODE == 2 ? kNK * kBN * 4 : 0);
-    static constexpr uint32_t kBar = kVs + (MODE == 2 ? kNV * kBN * 4 : 0);
-    static constexpr uint32_t kMl = kBar + 256;  // [2][kRows] fp32: maxima and sums of the copies
-    // results leave through [kRows][kOutCols + 4] floats over Q, free by then
-    static constexpr int kOutCols = D / 4;
-    static constexpr uint32_t kBytes = kMl + 2 * kRows * 4;
-    static constexpr uint32_t kMin = 80u * 1024u;  // at most two CTAs per SM (tensor memory has room for two)
-    static constexpr uint32_t kAlloc = (kBytes + 1024 > kMin ? kBytes + 1024 : kMin);  // + base alignment
-    static_assert(kRows * (kOutCols + 4) * 4 <= kQBytes, "results fit");
+    static constexpr uint32_t kBar = kVs + (MODE == 2 ? kNR * kBN * 4 : 0);
+    static constexpr uint32_t kMl = kBar + 512;  // [2][kUnitRows] fp32: maxima and sums of the copies
+    static constexpr uint32_t kOut = kMl + 2 * kUnitRows * 4;  // [kUnitRows][kOutStride] fp32: 16 columns of the copies
+    static constexpr int kOutStride = 20;
+    static constexpr uint32_t kBytes = kOut + kUnitRows * kOutStride * 4;
+    static constexpr uint32_t kMin = (NT == 1 ? 80u : 120u) * 1024u;  // no more CTAs per SM than tensor memory has room for
+    static constexpr uint32_t kAlloc = kBytes + 1024 > kMin ? kBytes + 1024 : kMin;  // + base alignment
+    static_assert(kCtasPerSm * (kAlloc + 1024) <= 228u * 1024u, "shared memory");
 };
 
+template <int NT>
 struct TreeBars {
     uint64_t q_full;
-    uint64_t k_full[kNK], k_empty[kNK];
-    uint64_t v_full[kNV], v_empty[kNV];      // the tile P V reads
-    uint64_t raw_full[kNV], raw_empty[kNV];  // E4M3 V codes
-    uint64_t s_full[2];
-    uint64_t p_full[2];
-    uint64_t pv_done;  // per tile; S(j) done and P of tile j missing leave it in phase j - 1 or j
-    uint64_t o_done;   // per unit, after its last tile
+    uint64_t k_full[4], k_empty[4];
+    uint64_t v_full[4], v_empty[4];  // the tile P V reads
+    uint64_t r_full[4], r_empty[4];  // E4M3 V codes
+    uint64_t s_full[NT][2];
+    uint64_t p_full[NT][2];
+    uint64_t pv_done[NT];  // per tile; S(j) done and P of tile j missing leave it in phase j - 1 or j
+    uint64_t o_done[NT];   // per unit, after its last tile
     uint64_t drained;
     uint32_t tmem;
     int nonfinite[2];  // by unit parity: a draft's V held an infinity or NaN
     int bad[2];        // by unit parity: a block id outside the pool
     int failed;        // a softmax wait gave up
-    long long scan[9]; // share computation
+    long long scan[16];  // share computation
 };
-static_assert(sizeof(TreeBars) <= 256, "barrier space");
+static_assert(sizeof(TreeBars<2>) <= 512, "barrier space");
 
 // 16-byte chunk c of row r in an operand of `D`-byte rows (E4M3): the 128-byte
 // swizzle (D 128) or the 64-byte one (D 64: chunk c of row r at c ^ (r / 2 % 4)).
@@ -180,7 +190,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&w)[8])
 }
 
 // Cost of a unit besides its tiles (query loads, first scores, results), in tiles.
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 4;
 // Shares are at least this long where the number of shares is chosen here: a
 // shorter one spends most of its time starting and joining.
 constexpr int kMinShare = 4;
@@ -204,15 +214,15 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int s, int log2_g) {
     q.invalid = !q.lost && q.c > 0 && (q.c > a.max_q_len || q.ctx < q.c || q.ctx > a.max_context_len);
     const bool work = !q.lost && !q.invalid && q.c > 0;
     q.tiles = work ? (q.ctx + kBN - 1) / kBN : 0;
-    q.row_tiles = work ? ((q.c << log2_g) + kRows - 1) / kRows : 0;
+    q.row_tiles = work ? ((q.c << log2_g) + a.unit_rows - 1) / a.unit_rows : 0;
     return q;
 }
 
 // What a CTA works on at a time; the same in every thread.
 struct Unit {
     int s, kh, q0, c, ctx, base;
-    int row0;    // first row (draft * G + head) of the tile
-    int rows;    // live rows of the tile
+    int row0;    // first row (draft * G + head)
+    int rows;    // live rows
     int per_copy, copies;
     int t0, t1;  // its keys here
     int tiles;   // and their tiles
@@ -227,64 +237,63 @@ struct Shares {
     __device__ __forceinline__ long long begin(int b) const { return total * b / shares; }
 };
 
-// Total cost (every thread of the block; `scratch` is shared memory for 9 values).
+// The total cost, and the sequence that holds the border `index` of the shares
+// (its begin) with the cost before it; for every thread of the block. `scratch`
+// is shared memory for 16 values.
 template <int THREADS>
-__device__ __forceinline__ Shares count_shares(const TreeArgs &a, int log2_g, long long *scratch) {
-    long long sum = 0;
-    for (int s = threadIdx.x; s < a.num_seqs; s += THREADS) sum += load_seq(a, s, log2_g).cost(a.num_kv_heads);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    Shares r;
-    r.total = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) r.total += scratch[w];
-    const long long most = r.total / a.min_share;
-    r.shares = static_cast<int>(most < 1 ? 1 : most < a.max_shares ? most : a.max_shares);
-    __syncthreads();
-    return r;
-}
-
-// The sequence that holds cost x < total, and the cost before it.
-template <int THREADS>
-__device__ __forceinline__ int find_seq(const TreeArgs &a, int log2_g, long long x, long long *scratch,
-                                        long long &before) {
+__device__ __forceinline__ Shares find_share(const TreeArgs &a, int log2_g, int index, long long *scratch, int &seq,
+                                             long long &before) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    long long done = 0;
-    for (int s0 = 0;; s0 += THREADS) {
-        const int s = s0 + threadIdx.x;
-        const long long cost = s < a.num_seqs ? load_seq(a, s, log2_g).cost(a.num_kv_heads) : 0;
-        long long inc = cost;
+    Shares sh;
+    sh.total = 0;
+    sh.shares = 1;
+    long long at = 0, cost = 0, done = 0, x = -1;
+    const int chunks = (a.num_seqs + THREADS - 1) / THREADS;
+    seq = 0;
+    before = 0;
+    // first round: the total (with one chunk of sequences the border is then
+    // looked for at once); second round: the border's chunk
+    for (int i = 0; i < 2 * chunks; ++i) {
+        const int s = (i < chunks ? i : i - chunks) * THREADS + threadIdx.x;
+        if (chunks > 1 || i == 0) {
+            if (i == chunks) done = 0;
+            cost = s < a.num_seqs ? load_seq(a, s, log2_g).cost(a.num_kv_heads) : 0;
+            long long inc = cost;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            if (lane == 31) scratch[warp] = inc;
+            __syncthreads();
+            at = done + inc;  // cost up to and with this sequence
+            for (int w = 0; w < THREADS / 32; ++w) {
+                const long long v = scratch[w];
+                if (w < warp) at += v;
+                done += v;
+            }
+            __syncthreads();
         }
-        if (lane == 31) scratch[warp] = inc;
-        __syncthreads();
-        long long at = done;
-        for (int w = 0; w < THREADS / 32; ++w) {
-            const long long v = scratch[w];
-            if (w < warp) at += v;
-            done += v;
+        if (i == chunks - 1) {
+            sh.total = done;
+            const long long most = done / a.min_share;
+            sh.shares = static_cast<int>(most < 1 ? 1 : most < a.max_shares ? most : a.max_shares);
+            if (done == 0 || index >= sh.shares) return sh;
+            x = sh.begin(index);
         }
-        at += inc;  // cost up to and with this sequence
-        const bool last = s0 + THREADS >= a.num_seqs;
-        const bool here = x < done || last;
-        __syncthreads();
-        if (here) {  // uniform: x lies in this chunk
-            if (s < a.num_seqs && x >= at - cost && x < at) {
+        if (i >= chunks && x < done) {  // uniform: the border lies in this chunk
+            if (x >= at - cost && x < at) {
                 scratch[0] = s;
                 scratch[1] = at - cost;
             }
             __syncthreads();
-            const int found = static_cast<int>(scratch[0]);
+            seq = static_cast<int>(scratch[0]);
             before = scratch[1];
             __syncthreads();
-            return found;
+            return sh;
         }
     }
+    return sh;
 }
 
 // Tiles of a unit of n tiles at cost p before cost x.
@@ -296,15 +305,16 @@ __device__ __forceinline__ int tiles_before(long long x, long long p, int n) {
 // Goes through the units of a share.
 struct Walk {
     long long x0, x1, p;  // the share, and the cost of the next unit
-    int s, k, share;
+    int s, k, share, rows;
     Seq q;
     __device__ __forceinline__ void start(const TreeArgs &a, const Shares &sh, int b, int seq, long long before,
-                                          int log2_g) {
+                                          int log2_g, int unit_rows) {
         share = b;
         x0 = sh.begin(b);
         x1 = sh.begin(b + 1);
         s = seq;
         q = load_seq(a, s, log2_g);
+        rows = unit_rows;
         k = static_cast<int>((x0 - before) / (q.tiles + kUnitCost));
         p = before + static_cast<long long>(k) * (q.tiles + kUnitCost);
     }
@@ -326,10 +336,10 @@ struct Walk {
             u.c = q.c;
             u.ctx = q.ctx;
             u.base = q.ctx - q.c;
-            u.row0 = (kk % q.row_tiles) * kRows;
-            u.rows = min(kRows, (q.c << log2_g) - u.row0);
-            u.per_copy = u.rows <= 32 ? 32 : u.rows <= 64 ? 64 : 128;
-            u.copies = kRows / u.per_copy;
+            u.row0 = (kk % q.row_tiles) * rows;
+            u.rows = min(rows, (q.c << log2_g) - u.row0);
+            u.copies = u.rows * 4 <= rows ? 4 : u.rows * 2 <= rows ? 2 : 1;
+            u.per_copy = rows / u.copies;
             u.t0 = tb * kBN;
             u.t1 = min(q.ctx, te * kBN);
             u.tiles = te - tb;
@@ -360,13 +370,13 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t *mask, int c, int s
 // V rows of the staged tile: rows at or past the end become zeros (zero_tail)
 // and elements that are not finite in the drafts' rows too; returns whether
 // there were any. F16: f16 elements, else bf16.
-template <int D, bool F16>
-__device__ __forceinline__ bool mend_v(uint32_t sv, int first, int end, bool zero_tail, int thread) {
+template <int D, bool F16, int THREADS>
+__device__ __forceinline__ bool mend_v(uint32_t sv, int first, int end, bool zero_tail) {
     constexpr int kChunks = D / 8;
     constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;
     bool found = false;
     const int last = zero_tail ? kBN : end;
-    for (int i = first * kChunks + thread; i < last * kChunks; i += kSoftmaxWarps * 32) {
+    for (int i = first * kChunks + threadIdx.x; i < last * kChunks; i += THREADS) {
         const int r = i / kChunks, c16 = i % kChunks;
         const uint32_t at = sv + swz(kBN, r, c16);
         if (r >= end) {
@@ -402,49 +412,61 @@ template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float p0, float p1) { return F16 ? pack_f16(p0, p1) : pack_bf16(p0, p1); }
 
 // Softmax of this warp's rows over the unit's tiles: 64 / copies keys of every
-// tile, 16 at a time in a loop (written out for 64 keys, in one variant per
+// tile, W at a time in a loop (written out for 64 keys, in one variant per
 // number of copies, the code outgrew the instruction cache: a CTA's first tile
 // took 8000 cycles). g0: tiles of the units before. Leaves the reference maximum
 // and the sum of the row (copy).
-template <int D, int MODE>
-__device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, TreeBars *bars, uint8_t *sm,
+template <int D, int MODE, int NT, int W>
+__device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, TreeBars<NT> *bars, uint8_t *sm,
                                               uint32_t base, uint32_t tmem, float sl2, bool live, int draft,
                                               uint32_t g0, int unit, float &m_out, float &l_out) {
-    using L = TreeLayout<D, MODE>;
-    constexpr bool kF16 = MODE == 1;
+    using L = Tree<D, MODE, NT>;
+    constexpr bool kF16 = L::kF16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const int half = warp >> 2;  // row tile
     const bool idle = !__any_sync(0xffffffffu, live);  // no row in this warp: its weights are never read
-    const int groups = 4 / u.copies;                   // of 16 keys
-    const int group0 = (warp * 32) / u.per_copy * groups;
+    const int cols = kBN / u.copies, col0 = (warp * 32) / u.per_copy * cols;
     const uint32_t *mask = a.mask + static_cast<long long>(u.q0 + draft) * a.mask_words;
-    const uint32_t to = tmem + 128 + lane_base;
+    const uint32_t tw = tmem + half * 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
+    const uint32_t to = tw + 128;
     float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
     for (int j = 0; j < u.tiles; ++j) {
         const uint32_t g = g0 + j;
         const int kv0 = u.t0 + j * kBN;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[g & 1], (g >> 1) & 1))) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[half][g & 1], (g >> 1) & 1))) return false;
         tc_fence_after();
         const bool special = kv0 + kBN > u.base;  // holds drafts, or keys past the end
         if (!idle) {
-            const uint32_t ts = tmem + (g & 1) * kBN + lane_base;
-            uint32_t next[16];
-            tmem_ld16(ts + 16 * group0, next);
-            if (MODE == 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->k_full[g % kNK], (g / kNK) & 1))) return false;
-            const float *ks = reinterpret_cast<const float *>(sm + L::kKs) + (g % kNK) * kBN;
+            const uint32_t ts = tw + (g & 1) * kBN;
+            uint32_t next[W / 16][16];
+#pragma unroll
+            for (int i = 0; i < W / 16; ++i) tmem_ld16(ts + col0 + 16 * i, next[i]);
+            if (MODE == 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->k_full[g % L::kNK], (g / L::kNK) & 1)))
+                return false;
+            const float *ks = reinterpret_cast<const float *>(sm + L::kKs) + (g % L::kNK) * kBN;
             float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-            for (int h = group0; h < group0 + groups; ++h) {
-                float x[16];
-                tmem_wait16(next);
+            for (int c = col0; c < col0 + cols; c += W) {
+                float x[W];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(next[i]) * sl2;
-                if (h + 1 < group0 + groups) tmem_ld16(ts + 16 * (h + 1), next);
+                for (int i = 0; i < W / 16; ++i) tmem_wait16(next[i]);
+#pragma unroll
+                for (int i = 0; i < W; i += 2) {
+                    const float2 y = __fmul2_rn(make_float2(__uint_as_float(next[i / 16][i % 16]),
+                                                            __uint_as_float(next[i / 16][i % 16 + 1])),
+                                                make_float2(sl2, sl2));
+                    x[i] = y.x;
+                    x[i + 1] = y.y;
+                }
+                if (c + W < col0 + cols) {
+#pragma unroll
+                    for (int i = 0; i < W / 16; ++i) tmem_ld16(ts + c + W + 16 * i, next[i]);
+                }
                 if constexpr (MODE == 2) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + 16 * h + i);
+                    for (int i = 0; i < W; i += 4) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + c + i);
                         x[i] *= k4.x;
                         x[i + 1] *= k4.y;
                         x[i + 2] *= k4.z;
@@ -452,14 +474,16 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                     }
                 }
                 if (special) {
-                    const uint32_t vis = live ? visible32(mask, u.c, kv0 + 16 * h, u.base) : 0u;
+                    const uint32_t vis = live ? visible32(mask, u.c, kv0 + c, u.base) : 0u;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
+                    for (int i = 0; i < W; ++i)
                         if (!((vis >> i) & 1u)) x[i] = -INFINITY;
                 }
                 float m4[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(x[k], x[k + 4]), fmaxf(x[k + 8], x[k + 12]));
+#pragma unroll
+                for (int i = 16; i < W; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 const bool grow = mx > m + 8.0f;
                 if (__any_sync(0xffffffffu, grow)) {
@@ -472,19 +496,19 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                         for (int k = 0; k < 4; ++k) l4[k] *= alpha;
                     }
 #pragma unroll 1
-                    for (int e = group0; e < h; ++e) {  // this tile's weights
+                    for (int e = col0; e < c; e += 16) {  // this tile's weights
                         uint32_t w[8];
-                        tmem_ld8(ts + 8 * e, w);
+                        tmem_ld8(ts + e / 2, w);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const __half2 f = *reinterpret_cast<const __half2 *>(&w[i]);
                             w[i] = pack_p<kF16>((kF16 ? __low2float(f) : bf16lo(w[i])) * alpha,
                                                 (kF16 ? __high2float(f) : bf16hi(w[i])) * alpha);
                         }
-                        tmem_st8(ts + 8 * e, w);
+                        tmem_st8(ts + e / 2, w);
                     }
                     if (j > 0) {  // S(j) done implies P V(j - 2) done: the next phase is P V(j - 1)
-                        if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (g - 1) & 1))) return false;
+                        if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[half], (g - 1) & 1))) return false;
                         tc_fence_after();
 #pragma unroll 1
                         for (int ch = 0; ch < D; ch += 8) {
@@ -496,44 +520,49 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.0f : m;  // nothing seen yet: weights exp2(-inf) = 0
-                uint32_t w[8];
+                const float ref = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: weights exp2(-inf) = 0
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    w[i] = pack_p<kF16>(fast_exp2(x[2 * i] - ref), fast_exp2(x[2 * i + 1] - ref));
-                    l4[i & 3] = kF16 ? fma_f16x2_acc(w[i], 0x3C003C00u, l4[i & 3])
-                                     : fma_bf16x2_acc(w[i], 0x3F803F80u, l4[i & 3]);
+                for (int h = 0; h < W / 16; ++h) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = __fadd2_rn(make_float2(x[16 * h + 2 * i], x[16 * h + 2 * i + 1]),
+                                                    make_float2(ref, ref));
+                        w[i] = pack_p<kF16>(fast_exp2(y.x), fast_exp2(y.y));
+                        l4[i & 3] = kF16 ? fma_f16x2_acc(w[i], 0x3C003C00u, l4[i & 3])
+                                         : fma_bf16x2_acc(w[i], 0x3F803F80u, l4[i & 3]);
+                    }
+                    tmem_st8(ts + c / 2 + 8 * h, w);
                 }
-                tmem_st8(ts + 8 * h, w);
             }
             l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-            if (groups < 4) {  // the other copies' keys
+            if (cols < kBN) {  // the other copies' keys
                 const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                for (int h = groups; h < 4; ++h) tmem_st8(ts + ((8 * (group0 + h)) & 31), zero);
+                for (int c = cols / 2; c < kBN / 2; c += 8) tmem_st8(ts + ((col0 / 2 + c) & 31), zero);
             }
         }
         if constexpr (MODE == 2) {
             // here, behind instructions that used every lane's scales: released right
             // after the loads, the slot was refilled under lanes still reading it
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->k_empty[g % kNK]);
+            if (lane == 0) mbar_arrive(&bars->k_empty[g % L::kNK]);
         }
         if (special) {
-            const int slot = g % kNV;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[slot], (g / kNV) & 1))) return false;
+            const uint32_t slot = g % L::kNV;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[slot], (g / L::kNV) & 1))) return false;
             const int first = max(0, u.base - kv0), end = min(kBN, u.ctx - kv0);
-            if (mend_v<D, kF16>(base + L::kV + slot * L::kVSlot, first, end, MODE == 0, threadIdx.x))
+            if (mend_v<D, kF16, L::kSoftmaxThreads>(base + L::kV + slot * L::kVSlot, first, end, MODE == 0))
                 bars->nonfinite[unit & 1] = 1;
             fence_proxy_async_smem();
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[g & 1]);
+        if (lane == 0) mbar_arrive(&bars->p_full[half][g & 1]);
     }
     // a barrier of its own: pv_done may be one or two phases further by now, and
     // a parity cannot tell which
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_done, unit & 1))) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_done[half], unit & 1))) return false;
     tc_fence_after();
     m_out = m;
     l_out = l;
@@ -575,128 +604,228 @@ __device__ __forceinline__ void add_nonfinite(const TreeArgs &a, const Unit &u, 
     for (int i = 0; i < N; ++i) v[i] = t[i];
 }
 
-// Results of a unit: the copies joined, normalised, written through shared
-// memory so that lanes write neighbouring elements: bf16 output, or the
-// binary32 partial (and maximum and sum) of a cut unit.
-template <int D, int MODE>
-__device__ __forceinline__ void write_unit(const TreeArgs &a, const Unit &u, TreeBars *bars, uint8_t *sm, uint32_t tmem,
-                                           int unit, int log2_g, bool ok, float m, float l) {
-    using L = TreeLayout<D, MODE>;
-    constexpr int kCols = L::kOutCols, kStride = kCols + 4;
-    const int tid = threadIdx.x, G = 1 << log2_g;
-    const int r = tid & (u.per_copy - 1);
+// N result elements (a multiple of 4) from column col of a unit's row: bf16
+// output, or the binary32 partial of a cut unit.
+template <int D, int MODE, int N>
+__device__ __forceinline__ void emit(const TreeArgs &a, const Unit &u, bool nonfinite, int draft, __nv_bfloat16 *out,
+                                     float *part, int col, float (&v)[N]) {
+    if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, col, v);
+    if (u.slot < 0) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        if constexpr (N % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < N / 2; i += 4)
+                *reinterpret_cast<uint4 *>(out + col + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; i += 2) *reinterpret_cast<uint2 *>(out + col + 2 * i) = make_uint2(w[i], w[i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4 *>(part + col + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
+
+// Results of a unit: normalised, the copies joined (through shared memory, 16
+// columns at a time), written as bf16 or as the partial, maximum and sum of a
+// cut unit.
+template <int D, int MODE, int NT>
+__device__ __forceinline__ void write_unit(const TreeArgs &a, const Unit &u, TreeBars<NT> *bars, uint8_t *sm,
+                                           uint32_t tmem, int unit, int log2_g, bool ok, float m, float l) {
+    using L = Tree<D, MODE, NT>;
+    constexpr int kUnitRows = L::kUnitRows, kThreads = L::kSoftmaxThreads;
+    const int tid = threadIdx.x, warp = tid >> 5, G = 1 << log2_g;
+    const int r = tid & (u.per_copy - 1), copy = tid / u.per_copy;
     float *ml = reinterpret_cast<float *>(sm + L::kMl);
-    float *o = reinterpret_cast<float *>(sm + L::kQ);
+    float *o = reinterpret_cast<float *>(sm + L::kOut);
     ml[tid] = m;
-    ml[kRows + tid] = ok ? l : 0.0f;
-    named_sync(1, kSoftmaxWarps * 32);  // (also: the flags are complete)
-    const bool nonfinite = bars->nonfinite[unit & 1] != 0, bad = bars->bad[unit & 1] != 0;
+    ml[kUnitRows + tid] = ok ? l : 0.0f;
+    named_sync(1, kThreads);  // (also: the flags are complete)
+    const bool bad = bars->bad[unit & 1] != 0, nonfinite = bars->nonfinite[unit & 1] != 0 && !bad;
     float top = -INFINITY, sum = 0.0f;
     for (int k = 0; k < u.copies; ++k) top = fmaxf(top, ml[k * u.per_copy + r]);
     const float ref = top == -INFINITY ? 0.0f : top;
     for (int k = 0; k < u.copies; ++k)
-        sum = fmaf(fast_exp2(ml[k * u.per_copy + r] - ref), ml[kRows + k * u.per_copy + r], sum);
+        sum = fmaf(fast_exp2(ml[k * u.per_copy + r] - ref), ml[kUnitRows + k * u.per_copy + r], sum);
     // a copy (or row) that saw nothing, and a bad unit, contribute zeros whatever O holds
     const bool drop = l == 0.0f || sum == 0.0f || bad || !ok;
     const float f = drop ? 0.0f : fast_exp2(m - ref) * ((MODE == 1 ? __ldg(a.v_scale + u.kh) : 1.0f) / sum);
-    const long long slot_rows = min(static_cast<long long>(kRows), static_cast<long long>(a.max_q_len) << log2_g);
-    if (u.slot >= 0 && tid < u.rows)
-        *reinterpret_cast<float2 *>(a.part_ml + (u.slot * slot_rows + tid) * 2) = make_float2(top, bad ? -1.0f : sum);
-    const uint32_t tmem_o = tmem + 128 + (static_cast<uint32_t>((tid >> 5) * 32) << 16);
+    const bool live = r < u.rows;
+    const int row = u.row0 + (live ? r : 0), draft = row >> log2_g;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
+                         (static_cast<long long>(u.q0 + draft) * a.num_q_heads + u.kh * G + (row & (G - 1))) * D;
+    const long long prow = static_cast<long long>(u.slot) * a.slot_rows + r;
+    float *part = a.part_o + prow * D;
+    if (u.slot >= 0 && live && copy == 0)
+        *reinterpret_cast<float2 *>(a.part_ml + prow * 2) = make_float2(top, bad ? -1.0f : sum);
+    const uint32_t to = tmem + (warp >> 2) * 256 + 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll 1
-    for (int ch = 0; ch < D / kCols; ++ch) {
+    for (int col = 0; col < D; col += 16) {
+        uint32_t w[16];
+        float v[16];
+        tmem_ld16(to + col, w);
+        tmem_wait16(w);
 #pragma unroll
-        for (int i0 = 0; i0 < kCols; i0 += 16) {
-            uint32_t v[16];
-            tmem_ld16(tmem_o + ch * kCols + i0, v);
-            tmem_wait16(v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = drop ? 0u : __float_as_uint(__uint_as_float(v[i]) * f);
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<uint4 *>(o + tid * kStride + i0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        for (int i = 0; i < 16; ++i) v[i] = drop ? 0.0f : __uint_as_float(w[i]) * f;
+        if (u.copies == 1) {
+            if (live) emit<D, MODE>(a, u, nonfinite, draft, out, part, col, v);
+            continue;
         }
-        named_sync(1, kSoftmaxWarps * 32);
-        constexpr int kPer = kCols / 8;  // 8 columns a thread
-        for (int i = tid; i < u.rows * kPer; i += kSoftmaxWarps * 32) {
-            const int rr = i / kPer, col = (i % kPer) * 8;
-            const int row = u.row0 + rr, draft = row >> log2_g, head = u.kh * G + (row & (G - 1));
-            float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                float4 y = *reinterpret_cast<const float4 *>(o + rr * kStride + col + e);
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4 *>(o + tid * L::kOutStride + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        named_sync(1, kThreads);
+        if (live) {
+            // 16 columns of the row, 4 at a time over the copies' threads
+            for (int c4 = copy; c4 < 4; c4 += u.copies) {
+                float4 y = *reinterpret_cast<const float4 *>(o + r * L::kOutStride + 4 * c4);
                 for (int k = 1; k < u.copies; ++k) {
-                    const float4 z = *reinterpret_cast<const float4 *>(o + (k * u.per_copy + rr) * kStride + col + e);
+                    const float4 z =
+                        *reinterpret_cast<const float4 *>(o + (k * u.per_copy + r) * L::kOutStride + 4 * c4);
                     y.x += z.x;
                     y.y += z.y;
                     y.z += z.z;
                     y.w += z.w;
                 }
-                x[e] = y.x;
-                x[e + 1] = y.y;
-                x[e + 2] = y.z;
-                x[e + 3] = y.w;
-            }
-            if (nonfinite && !bad) add_nonfinite<D, MODE>(a, u, draft, ch * kCols + col, x);
-            if (u.slot < 0) {
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                     (static_cast<long long>(u.q0 + draft) * a.num_q_heads + head) * D + ch * kCols + col;
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                                             pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-            } else {
-                float *dst = a.part_o + (u.slot * slot_rows + rr) * D + ch * kCols + col;
-                *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                float x[4] = {y.x, y.y, y.z, y.w};
+                emit<D, MODE>(a, u, nonfinite, draft, out, part, col + 4 * c4, x);
             }
         }
-        named_sync(1, kSoftmaxWarps * 32);
+        named_sync(1, kThreads);
     }
+    named_sync(1, kThreads);  // the flags are read
     if (tid == 0) {
         if (bad) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
-        bars->nonfinite[unit & 1] = 0;  // read by everyone above; next used two units on
+        bars->nonfinite[unit & 1] = 0;  // next used two units on
         bars->bad[unit & 1] = 0;
     }
 }
 
-template <int D, int MODE>
-__global__ void __launch_bounds__(tree_threads<MODE>(), 2)
+// The unit's queries into shared memory (every copy of a row), the softmax
+// scale of this thread's row, and the check of the unit's block ids.
+template <int D, int MODE, int NT>
+__device__ __forceinline__ float load_queries(const TreeArgs &a, const Unit &u, TreeBars<NT> *bars, uint32_t base,
+                                              int unit, int log2_g, int log2_bs) {
+    using L = Tree<D, MODE, NT>;
+    constexpr int kChunks = D / 8;
+    const int tid = threadIdx.x, G = 1 << log2_g;
+    float sl2 = a.scale * kLog2e;
+    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q);
+    auto row_of = [&](int row) {
+        return (static_cast<long long>(u.q0 + (row >> log2_g)) * a.num_q_heads + u.kh * G + (row & (G - 1))) * D;
+    };
+    if constexpr (!L::kFp8) {
+        for (int i = tid; i < L::kUnitRows * kChunks; i += L::kSoftmaxThreads) {
+            const int p = i / kChunks, c16 = i % kChunks;
+            const int r = p & (u.per_copy - 1);
+            const bool ok = r < u.rows;
+            cp_async16(base + L::kQ + (p / kRows) * L::kQTile + swz(kRows, p % kRows, c16),
+                       qp + row_of(u.row0 + (ok ? r : 0)) + c16 * 8, ok ? 16u : 0u);
+        }
+        cp_async_commit();
+    } else {
+        const int r = tid & (u.per_copy - 1);
+        const bool live = r < u.rows;
+        const uint4 *qrow = reinterpret_cast<const uint4 *>(qp + row_of(u.row0 + (live ? r : 0)));
+        float amax = 0.0f;
+        if (live) {
+#pragma unroll 8
+            for (int c16 = 0; c16 < kChunks; ++c16) {
+                const uint4 v4 = __ldg(qrow + c16);
+                const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
+            }
+        }
+        // amax < 2^e; times 2^kq it lies in [2^7, 2^8). kq is capped at 60 so that
+        // 2^-kq times the softmax scale stays normal: rows that small have scores
+        // of zero to binary32 against any finite key.
+        const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 126;
+        const int kq = min(60, 8 - e);
+        const float qs = __int_as_float((kq + 127) << 23);
+        sl2 *= __int_as_float((127 - kq) << 23);
+        if (MODE == 1) sl2 *= __ldg(a.k_scale + u.kh);
+        if (!(amax <= 3.4e38f)) sl2 = __int_as_float(0x7FC00000);  // an infinite query: E4M3 has none
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {  // 16 elements: one chunk of hi and of lo
+            const uint4 v0 = live ? __ldg(qrow + 2 * c) : make_uint4(0, 0, 0, 0);
+            const uint4 v1 = live ? __ldg(qrow + 2 * c + 1) : make_uint4(0, 0, 0, 0);
+            const uint32_t wv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float x = bf16lo(wv[k]) * qs, y = bf16hi(wv[k]) * qs;
+                const uint16_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+                const float2 hf = e4m3x2_to_float2(h);
+                const uint16_t o = __nv_cvt_float2_to_fp8x2(make_float2(x - hf.x, y - hf.y), __NV_SATFINITE, __NV_E4M3);
+                if (k & 1) {
+                    hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
+                    lo[k >> 1] |= static_cast<uint32_t>(o) << 16;
+                } else {
+                    hi[k >> 1] = h;
+                    lo[k >> 1] = o;
+                }
+            }
+            const uint32_t at = base + L::kQ + (tid / kRows) * L::kQTile + swz8<D>(tid % kRows, c);
+            st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            st_shared16(at + kRows * D, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+    }
+    // the producer copies block 0 in place of an id outside the pool; the results become zeros
+    const int32_t *table = a.block_tables + static_cast<long long>(u.s) * a.max_blocks_per_seq;
+    for (int i = (u.t0 >> log2_bs) + tid; i <= (u.t1 - 1) >> log2_bs; i += L::kSoftmaxThreads) {
+        const int id = __ldg(table + i);
+        if (id < 0 || id >= a.num_blocks) bars->bad[unit & 1] = 1;
+    }
+    if constexpr (!L::kFp8) cp_async_wait0();
+    fence_proxy_async_smem();
+    mbar_arrive(&bars->q_full);
+    return sl2;
+}
+
+template <int D, int MODE, int NT>
+__global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>::kCtasPerSm)
     tree_kernel(const __grid_constant__ TreeArgs a, int log2_bs, int log2_g, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
-    using L = TreeLayout<D, MODE>;
-    constexpr bool kFp8 = MODE != 0;
-    constexpr int kThreads = tree_threads<MODE>();
+    using L = Tree<D, MODE, NT>;
+    constexpr bool kFp8 = L::kFp8;
+    constexpr int kThreads = L::kThreads;
+    constexpr uint32_t kNK = L::kNK, kNV = L::kNV, kNR = L::kNR;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *sm = smem_raw + (base - raw);
-    TreeBars *bars = reinterpret_cast<TreeBars *>(sm + L::kBar);
+    TreeBars<NT> *bars = reinterpret_cast<TreeBars<NT> *>(sm + L::kBar);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = 1 << log2_g, bs = a.block_size;
+    const int bs = a.block_size;
 
     // ------------------------------------------------ setup
-    if (warp == kMmaWarp) tmem_alloc(smem_addr(&bars->tmem), kTmemCols);
+    if (warp == L::kMmaWarp) tmem_alloc(smem_addr(&bars->tmem), L::kTmemCols);
     if (tid == 0) {
-        mbar_init(&bars->q_full, kSoftmaxWarps * 32);
-        for (int i = 0; i < kNK; ++i) {
+        mbar_init(&bars->q_full, L::kSoftmaxThreads);
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&bars->k_full[i], 1);
-            mbar_init(&bars->k_empty[i], MODE == 2 ? 1 + kSoftmaxWarps : 1);  // the scales are read by the softmax
-        }
-        for (int i = 0; i < kNV; ++i) {
-            mbar_init(&bars->v_full[i], kFp8 ? kConvWarps : 1);
+            mbar_init(&bars->k_empty[i], MODE == 2 ? 1 + L::kSoftmaxWarps : 1);  // the softmax reads the scales
+            mbar_init(&bars->v_full[i], kFp8 ? L::kConvWarps : 1);
             mbar_init(&bars->v_empty[i], 1);
-            mbar_init(&bars->raw_full[i], 1);
-            mbar_init(&bars->raw_empty[i], kConvWarps);
+            mbar_init(&bars->r_full[i], 1);
+            mbar_init(&bars->r_empty[i], L::kConvWarps);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_full[i], kSoftmaxWarps);
-            bars->nonfinite[i] = 0;
-            bars->bad[i] = 0;
+        for (int x = 0; x < NT; ++x) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&bars->s_full[x][i], 1);
+                mbar_init(&bars->p_full[x][i], 4);
+            }
+            mbar_init(&bars->pv_done[x], 1);
+            mbar_init(&bars->o_done[x], 1);
         }
-        bars->failed = 0;
-        mbar_init(&bars->pv_done, 1);
-        mbar_init(&bars->o_done, 1);
         mbar_init(&bars->drained, 1);
+        bars->nonfinite[0] = bars->nonfinite[1] = 0;
+        bars->bad[0] = bars->bad[1] = 0;
+        bars->failed = 0;
         fence_barrier_init();
     }
     // sequences that cannot be served: reported, and zeros where their rows can be located
@@ -709,117 +838,51 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
             for (long long i = tid; i < n; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    const Shares sh = count_shares<kThreads>(a, log2_g, bars->scan);
+    const int share = blockIdx.x;
+    int seq;
+    long long before;
+    const Shares sh = find_share<kThreads>(a, log2_g, share, bars->scan, seq, before);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
-    const int share = blockIdx.x;
     const bool work = sh.total > 0 && share < sh.shares;
     Walk walk;
     Unit u;
     uint32_t g = 0;  // tiles of the units before
-    if (work) {
-        long long before;
-        const int s = find_seq<kThreads>(a, log2_g, sh.begin(share), bars->scan, before);
-        walk.start(a, sh, share, s, before, log2_g);
-    }
+    if (work) walk.start(a, sh, share, seq, before, log2_g, L::kUnitRows);
 
     if (!work) {
         // more CTAs than shares
-    } else if (warp < kSoftmaxWarps) {
+    } else if (warp < L::kSoftmaxWarps) {
         // ================================================ softmax
-        for (int unit = 0; walk.next(a, log2_g, u); ++unit) {
-            // this thread's row: copy tid / per_copy
+        bool more = walk.next(a, log2_g, u);
+        float sl2 = more ? load_queries<D, MODE, NT>(a, u, bars, base, 0, log2_g, log2_bs) : 0.0f;
+        for (int unit = 0; more; ++unit) {
+            // this thread's row (of copy tid / per_copy)
             const int r = tid & (u.per_copy - 1);
             const bool live = r < u.rows;
-            const int row = u.row0 + (live ? r : 0);
-            const int draft = row >> log2_g, head = u.kh * G + (row & (G - 1));
-            const int32_t *table = a.block_tables + static_cast<long long>(u.s) * a.max_blocks_per_seq;
-            float sl2 = a.scale * kLog2e;
-            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q);
-            constexpr int kChunks = D / 8;
-            if constexpr (!kFp8) {
-                for (int i = tid; i < kRows * kChunks; i += kRows) {
-                    const int p = i / kChunks, c16 = i % kChunks;
-                    const int pr = p & (u.per_copy - 1);
-                    const bool ok = pr < u.rows;
-                    const int rr = u.row0 + (ok ? pr : 0);
-                    const long long e = (static_cast<long long>(u.q0 + (rr >> log2_g)) * a.num_q_heads + u.kh * G +
-                                         (rr & (G - 1))) * D + c16 * 8;
-                    cp_async16(base + L::kQ + swz(kRows, p, c16), qp + e, ok ? 16u : 0u);
-                }
-                cp_async_commit();
-                cp_async_wait0();
-            } else {
-                const uint4 *qrow = reinterpret_cast<const uint4 *>(
-                    qp + (static_cast<long long>(u.q0 + draft) * a.num_q_heads + head) * D);
-                float amax = 0.0f;
-                if (live) {
-#pragma unroll 8
-                    for (int c16 = 0; c16 < kChunks; ++c16) {
-                        const uint4 v4 = __ldg(qrow + c16);
-                        const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
-                    }
-                }
-                // amax < 2^e; times 2^kq it lies in [2^7, 2^8). kq is capped at 60
-                // so that 2^-kq times the softmax scale stays normal: rows that
-                // small have scores of zero to binary32 against any finite key.
-                const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 126;
-                const int kq = min(60, 8 - e);
-                const float qs = __int_as_float((kq + 127) << 23);
-                sl2 *= __int_as_float((127 - kq) << 23);
-                if (MODE == 1) sl2 *= __ldg(a.k_scale + u.kh);
-                if (!(amax <= 3.4e38f)) sl2 = __int_as_float(0x7FC00000);  // an infinite query: E4M3 has none
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {  // 16 elements: one chunk of hi and of lo
-                    const uint4 v0 = live ? __ldg(qrow + 2 * c) : make_uint4(0, 0, 0, 0);
-                    const uint4 v1 = live ? __ldg(qrow + 2 * c + 1) : make_uint4(0, 0, 0, 0);
-                    const uint32_t wv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float x = bf16lo(wv[k]) * qs, y = bf16hi(wv[k]) * qs;
-                        const uint16_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-                        const float2 hf = e4m3x2_to_float2(h);
-                        const uint16_t o =
-                            __nv_cvt_float2_to_fp8x2(make_float2(x - hf.x, y - hf.y), __NV_SATFINITE, __NV_E4M3);
-                        if (k & 1) {
-                            hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
-                            lo[k >> 1] |= static_cast<uint32_t>(o) << 16;
-                        } else {
-                            hi[k >> 1] = h;
-                            lo[k >> 1] = o;
-                        }
-                    }
-                    const uint32_t at = base + L::kQ + swz8<D>(tid, c);
-                    st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    st_shared16(at + kRows * D, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                }
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&bars->q_full);
-            // the producer copies block 0 in place of an id outside the pool; the results become zeros
-            for (int i = (u.t0 >> log2_bs) + tid; i <= (u.t1 - 1) >> log2_bs; i += kRows) {
-                const int id = __ldg(table + i);
-                if (id < 0 || id >= a.num_blocks) bars->bad[unit & 1] = 1;
-            }
+            const int draft = (u.row0 + (live ? r : 0)) >> log2_g;
             float m = -INFINITY, l = 0.0f;
-            const bool ok =
-                softmax_tiles<D, MODE>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
+            const bool ok = u.copies == 4 ? softmax_tiles<D, MODE, NT, 16>(a, u, bars, sm, base, tmem, sl2, live, draft,
+                                                                           g, unit, m, l)
+                                          : softmax_tiles<D, MODE, NT, 32>(a, u, bars, sm, base, tmem, sl2, live, draft,
+                                                                           g, unit, m, l);
             if (!ok && lane == 0) {
                 set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
                 bars->failed = 1;
             }
             g += u.tiles;
-            write_unit<D, MODE>(a, u, bars, sm, tmem, unit, log2_g, ok, m, l);
+            // O is complete, so every S is: the next queries may replace these
+            Unit next;
+            more = walk.next(a, log2_g, next);
+            if (more) sl2 = load_queries<D, MODE, NT>(a, next, bars, base, unit + 1, log2_g, log2_bs);
+            write_unit<D, MODE, NT>(a, u, bars, sm, tmem, unit, log2_g, ok, m, l);
             if (bars->failed) break;  // written before a barrier of write_unit: the same for all
+            u = next;
         }
         __syncwarp();
-    } else if (warp == kProducerWarp) {
+    } else if (warp == L::kProducerWarp) {
         // ================================================ producer
         constexpr int kHalves = D / 64;
         bool ok = true;
@@ -849,9 +912,10 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                 const bool mine = bi < n;
                 const uint32_t t = g + j;
                 auto stage = [&](bool is_k) -> bool {
-                    const uint32_t slot = is_k ? t % kNK : t % kNV, use = is_k ? t / kNK : t / kNV;
-                    uint64_t *empty = is_k ? &bars->k_empty[slot] : kFp8 ? &bars->raw_empty[slot] : &bars->v_empty[slot];
-                    uint64_t *full = is_k ? &bars->k_full[slot] : kFp8 ? &bars->raw_full[slot] : &bars->v_full[slot];
+                    constexpr uint32_t kN2 = kFp8 ? kNR : kNV;
+                    const uint32_t slot = is_k ? t % kNK : t % kN2, use = is_k ? t / kNK : t / kN2;
+                    uint64_t *empty = is_k ? &bars->k_empty[slot] : kFp8 ? &bars->r_empty[slot] : &bars->v_empty[slot];
+                    uint64_t *full = is_k ? &bars->k_full[slot] : kFp8 ? &bars->r_full[slot] : &bars->v_full[slot];
                     if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (use - 1) & 1))) return false;
                     const uint32_t bytes = static_cast<uint32_t>(n * run) * (D * (kFp8 ? 1 : 2) + (MODE == 2 ? 4 : 0));
                     if (lane == 0) mbar_arrive_expect_tx(full, bytes);
@@ -866,7 +930,7 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                                 tma_load_2d(base + L::kK + slot * L::kKSlot + bi * run * D, &map_k, 0,
                                             static_cast<int>(prow), full);
                             else
-                                bulk_g2s(sm + L::kRaw + slot * L::kRawSlot + bi * run * D,
+                                bulk_g2s(sm + L::kR + slot * L::kRSlot + bi * run * D,
                                          static_cast<const uint8_t *>(a.v_cache) + prow * D, run * D, full);
                             if constexpr (MODE == 2)
                                 bulk_g2s(sm + (is_k ? L::kKs : L::kVs) + slot * kBN * 4 + bi * run * 4,
@@ -890,39 +954,43 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
             // copies still in flight (only after a timeout): wait for them before the CTA exits
             for (uint32_t j = issued_k > kNK ? issued_k - kNK : 0; j < issued_k; ++j)
                 mbar_wait(&bars->k_full[j % kNK], (j / kNK) & 1);
-            for (uint32_t j = issued_v > kNV ? issued_v - kNV : 0; j < issued_v; ++j)
-                mbar_wait(kFp8 ? &bars->raw_full[j % kNV] : &bars->v_full[j % kNV], (j / kNV) & 1);
+            constexpr uint32_t kN2 = kFp8 ? kNR : kNV;
+            for (uint32_t j = issued_v > kN2 ? issued_v - kN2 : 0; j < issued_v; ++j)
+                mbar_wait(kFp8 ? &bars->r_full[j % kN2] : &bars->v_full[j % kN2], (j / kN2) & 1);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == L::kMmaWarp) {
         // ================================================ MMA issue
         if (lane == 0) {
             constexpr uint32_t kIdescS = kFp8 ? idesc_f16(kRows, kBN, false) : idesc_bf16(kRows, kBN, false);
             constexpr uint32_t kIdescPV = MODE == 1 ? idesc_f16(kRows, D, true) : idesc_bf16(kRows, D, true);
-            const uint32_t sq = base + L::kQ;
             auto issue_s = [&](uint32_t t) -> bool {
                 if (!mbar_wait(&bars->k_full[t % kNK], (t / kNK) & 1)) return false;
                 tc_fence_after();
                 const uint32_t sk = base + L::kK + (t % kNK) * L::kKSlot;
-                const uint32_t ts = tmem + (t & 1) * kBN;
-                if constexpr (kFp8) {  // E4M3: format code 0 for A and B, 32 elements per step; hi, then lo
+#pragma unroll 1
+                for (int x = 0; x < NT; ++x) {
+                    const uint32_t sq = base + L::kQ + x * L::kQTile;
+                    const uint32_t ts = tmem + x * 256 + (t & 1) * kBN;
+                    if constexpr (kFp8) {  // E4M3: format code 0 for A and B, 32 elements per step; hi, then lo
 #pragma unroll
-                    for (int kk = 0; kk < 2 * (D / 32); ++kk) {
-                        const uint32_t off = static_cast<uint32_t>((kk % (D / 32)) * 32);
-                        mma_f8(ts, desc8<D>(sq + (kk / (D / 32)) * kRows * D + off), desc8<D>(sk + off), kIdescS,
-                               kk > 0 ? 1u : 0u);
-                    }
-                } else {
+                        for (int kk = 0; kk < 2 * (D / 32); ++kk) {
+                            const uint32_t off = static_cast<uint32_t>((kk % (D / 32)) * 32);
+                            mma_f8(ts, desc8<D>(sq + (kk / (D / 32)) * kRows * D + off), desc8<D>(sk + off), kIdescS,
+                                   kk > 0 ? 1u : 0u);
+                        }
+                    } else {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t ao = static_cast<uint32_t>((kk >> 2) * kRows * 128 + (kk & 3) * 32);
-                        const uint32_t bo = static_cast<uint32_t>((kk >> 2) * kBN * 128 + (kk & 3) * 32);
-                        mma_bf16(ts, sw128_desc(sq + ao, 16, 1024), sw128_desc(sk + bo, 16, 1024), kIdescS,
-                                 kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t ao = static_cast<uint32_t>((kk >> 2) * kRows * 128 + (kk & 3) * 32);
+                            const uint32_t bo = static_cast<uint32_t>((kk >> 2) * kBN * 128 + (kk & 3) * 32);
+                            mma_bf16(ts, sw128_desc(sq + ao, 16, 1024), sw128_desc(sk + bo, 16, 1024), kIdescS,
+                                     kk > 0 ? 1u : 0u);
+                        }
                     }
+                    if (x == NT - 1) mma_commit(&bars->k_empty[t % kNK]);
+                    mma_commit(&bars->s_full[x][t & 1]);
                 }
-                mma_commit(&bars->k_empty[t % kNK]);
-                mma_commit(&bars->s_full[t & 1]);
                 return true;
             };
             bool ok = true;
@@ -932,19 +1000,25 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                     const uint32_t t = g + j;
                     // the next tile's S buffer was P of tile j - 1, which P V(j - 1) read before
                     if (j + 1 < u.tiles) ok = issue_s(t + 1);
-                    ok = ok && mbar_wait(&bars->p_full[t & 1], (t >> 1) & 1) &&
-                         mbar_wait(&bars->v_full[t % kNV], (t / kNV) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
+                    ok = ok && mbar_wait(&bars->v_full[t % kNV], (t / kNV) & 1);
+                    // every softmax warp mends a part of the V of a tile with drafts
+                    if (NT > 1 && ok && u.t0 + (j + 1) * kBN > u.base)
+                        for (int x = 1; x < NT && ok; ++x) ok = mbar_wait(&bars->p_full[x][t & 1], (t >> 1) & 1);
                     const uint32_t sv = base + L::kV + (t % kNV) * L::kVSlot;
+#pragma unroll 1
+                    for (int x = 0; x < NT && ok; ++x) {
+                        ok = mbar_wait(&bars->p_full[x][t & 1], (t >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < kBN / 16; ++kk)
-                        mma_bf16_ts(tmem + 128, tmem + (t & 1) * kBN + kk * 8,
-                                    sw128_desc(sv + static_cast<uint32_t>(kk * 16 * 128), kBN * 128, 1024), kIdescPV,
-                                    (j > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(&bars->v_empty[t % kNV]);
-                    mma_commit(&bars->pv_done);
-                    if (j + 1 == u.tiles) mma_commit(&bars->o_done);
+                        for (int kk = 0; kk < kBN / 16; ++kk)
+                            mma_bf16_ts(tmem + x * 256 + 128, tmem + x * 256 + (t & 1) * kBN + kk * 8,
+                                        sw128_desc(sv + static_cast<uint32_t>(kk * 16 * 128), kBN * 128, 1024),
+                                        kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (x == NT - 1) mma_commit(&bars->v_empty[t % kNV]);
+                        mma_commit(&bars->pv_done[x]);
+                        if (j + 1 == u.tiles) mma_commit(&bars->o_done[x]);
+                    }
                 }
                 g += u.tiles;
             }
@@ -955,22 +1029,22 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
         }
         __syncwarp();
     } else if constexpr (kFp8) {
-        // ================================================ V converters (warps 6, 7)
-        constexpr int kCT = kConvWarps * 32;
+        // ================================================ V converters
+        constexpr int kCT = L::kConvWarps * 32;
         constexpr int kCPR = D / 16;  // 16-code chunks per row
-        const int ct = tid - 192;
+        const int ct = tid - 32 * L::kFirstConvWarp;
         bool ok = true;
         while (ok && walk.next(a, log2_g, u)) {
             for (int j = 0; j < u.tiles; ++j) {
-                const uint32_t t = g + j, slot = t % kNV;
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->raw_full[slot], (t / kNV) & 1)) ||
+                const uint32_t t = g + j, slot = t % kNV, rslot = t % kNR;
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->r_full[rslot], (t / kNR) & 1)) ||
                     (t >= kNV && !__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[slot], (t / kNV - 1) & 1)))) {
                     ok = false;
                     break;
                 }
                 const int end = min(kBN, u.t1 - (u.t0 + j * kBN));  // rows past the end become zeros
-                const uint8_t *src = sm + L::kRaw + slot * L::kRawSlot;
-                const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + slot * kBN;
+                const uint8_t *src = sm + L::kR + rslot * L::kRSlot;
+                const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + rslot * kBN;
                 const uint32_t dst = base + L::kV + slot * L::kVSlot;
 #pragma unroll 2
                 for (int i0 = 0; i0 < kBN * kCPR; i0 += kCT) {
@@ -997,7 +1071,7 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bars->v_full[slot]);
-                    mbar_arrive(&bars->raw_empty[slot]);
+                    mbar_arrive(&bars->r_empty[rslot]);
                 }
             }
             g += u.tiles;
@@ -1008,9 +1082,9 @@ __global__ void __launch_bounds__(tree_threads<MODE>(), 2)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == L::kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, L::kTmemCols);
     }
 }
 
@@ -1021,14 +1095,14 @@ constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int log2_g) {
-    __shared__ long long scratch[9];
+    __shared__ long long scratch[16];
     const int tid = threadIdx.x, G = 1 << log2_g;
-    const Shares sh = count_shares<kJoinThreads>(a, log2_g, scratch);
     const int border = blockIdx.x + 1;
-    if (border >= sh.shares) return;
-    const long long x = sh.begin(border);
+    int s;
     long long p;
-    const int s = find_seq<kJoinThreads>(a, log2_g, x, scratch, p);
+    const Shares sh = find_share<kJoinThreads>(a, log2_g, border, scratch, s, p);
+    if (sh.total == 0 || border >= sh.shares) return;
+    const long long x = sh.begin(border);
     const Seq q = load_seq(a, s, log2_g);
     const int k = static_cast<int>((x - p) / (q.tiles + kUnitCost));
     p += static_cast<long long>(k) * (q.tiles + kUnitCost);
@@ -1038,9 +1112,9 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     while (tiles_before(sh.begin(first), p, q.tiles) > 0) --first;
     while (end < sh.shares && tiles_before(sh.begin(end), p, q.tiles) < q.tiles) ++end;
     const int pieces = end - first, part = border - 1 - first, parts = pieces - 1;
-    const int kh = k / q.row_tiles, row0 = (k % q.row_tiles) * kRows;
-    const int rows = min(kRows, (q.c << log2_g) - row0);
-    const long long slot_rows = min(static_cast<long long>(kRows), static_cast<long long>(a.max_q_len) << log2_g);
+    const int kh = k / q.row_tiles, row0 = (k % q.row_tiles) * a.unit_rows;
+    const int rows = min(a.unit_rows, (q.c << log2_g) - row0);
+    const long long slot_rows = a.slot_rows;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
     // a unit's first piece is in its share's second slot, the others in the first ones
     auto slot = [&](int i) { return i == 0 ? 2LL * first + 1 : 2LL * (first + i); };
@@ -1096,9 +1170,9 @@ bool make_map(CUtensorMap *map, const void *pool, const TreeArgs &a) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int MODE>
+template <int D, int MODE, int NT>
 cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
-    using L = TreeLayout<D, MODE>;
+    using L = Tree<D, MODE, NT>;
     const int g = a.num_q_heads / a.num_kv_heads;
     int log2_bs = 0, log2_g = 0;
     while ((1 << log2_bs) < a.block_size) ++log2_bs;
@@ -1108,7 +1182,7 @@ cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
     CUtensorMap mk, mv;
     memset(&mv, 0, sizeof(mv));
     if (!make_map(&mk, a.k_cache, a) || (MODE == 0 && !make_map(&mv, a.v_cache, a))) return cudaErrorInvalidValue;
-    auto kern = tree_kernel<D, MODE>;
+    auto kern = tree_kernel<D, MODE, NT>;
     static std::atomic<unsigned long long> configured{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1119,7 +1193,7 @@ cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    kern<<<a.max_shares, tree_threads<MODE>(), L::kAlloc, stream>>>(a, log2_bs, log2_g, mk, mv);
+    kern<<<a.max_shares, L::kThreads, L::kAlloc, stream>>>(a, log2_bs, log2_g, mk, mv);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.max_shares == 1) return e;
     tree_join_kernel<D><<<a.max_shares - 1, kJoinThreads, 0, stream>>>(a, log2_g);
@@ -1128,18 +1202,36 @@ cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
+// One or two row tiles per unit: two once a tree may have more rows than a tile
+// (they share every key tile then, and the call is bound by more than its reads).
+int tree_unit_rows(int max_q_len, int group) {
+    return static_cast<long long>(max_q_len) * group > kRows ? 2 * kRows : kRows;
+}
+int tree_ctas_per_sm(int max_q_len, int group) { return tree_unit_rows(max_q_len, group) == kRows ? 2 : 1; }
 int tree_slot_rows(int max_q_len, int group) {
     const long long rows = static_cast<long long>(max_q_len) * group;
-    return rows < kRows ? static_cast<int>(rows) : kRows;
+    const int unit = tree_unit_rows(max_q_len, group);
+    return rows < unit ? static_cast<int>(rows) : unit;
 }
 int tree_min_share() { return kMinShare; }
 
+namespace {
+
+template <int D, int MODE>
+cudaError_t launch_rows(const TreeArgs &a, cudaStream_t stream) {
+    return a.unit_rows == kRows ? launch_mode<D, MODE, 1>(a, stream) : launch_mode<D, MODE, 2>(a, stream);
+}
+
+template <int D>
+cudaError_t launch_dim(const TreeArgs &a, cudaStream_t stream) {
+    return a.mode == 0 ? launch_rows<D, 0>(a, stream)
+                       : a.mode == 1 ? launch_rows<D, 1>(a, stream) : launch_rows<D, 2>(a, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
-    if (a.head_dim == 128)
-        return a.mode == 0 ? launch_mode<128, 0>(a, stream)
-                           : a.mode == 1 ? launch_mode<128, 1>(a, stream) : launch_mode<128, 2>(a, stream);
-    return a.mode == 0 ? launch_mode<64, 0>(a, stream)
-                       : a.mode == 1 ? launch_mode<64, 1>(a, stream) : launch_mode<64, 2>(a, stream);
+    return a.head_dim == 128 ? launch_dim<128>(a, stream) : launch_dim<64>(a, stream);
 }
 
 }  // namespace pkv

@@ -224,10 +224,10 @@ def test_tree_mask_helper(K):
 
 
 def test_tree_plan(K):
-    """The workspace holds two partials of up to 128 rows for every share."""
+    """The workspace holds two partials of up to 256 rows for every share."""
     for args in ((1, 32, 8, 128, 256, 8, 512), (64, 32, 8, 128, 16, 32, 32768), (1, 4, 4, 64, 8, 1, 1),
                  (3, 8, 1, 64, 1024, 300, 40000)):
-        rows = min(128, args[5] * args[1] // args[2])
+        rows = min(256, args[5] * args[1] // args[2])
         for dt in (K.PKV_CACHE_BF16, K.PKV_CACHE_FP8_E4M3, K.PKV_CACHE_FP8_E4M3_TOKEN):
             for shares in (0, 1, 2, 77, 4096):
                 p = K.plan_tree(*args, cache_dtype=dt, shares=shares)

@@ -49,8 +49,8 @@
 // converted. V is widened to f16 (exact) with a scale per KV head, where P is
 // rounded to f16, and to bf16(code * scale) with a scale per token, where P is
 // rounded to bf16 (V's range is then the scales'). The softmax runs in base 2
-// with a reference maximum that moves only when a tile exceeds it by 8, and the
-// normaliser sums the rounded weights.
+// with a reference maximum that moves only when a key exceeds it by 8; the normaliser
+// sums the weights in binary32 as they are before rounding.
 //
 // Masked keys: a score that the row does not see becomes -inf whatever it
 // was, so its weight is zero; and V elements of drafts that are not finite are
@@ -153,6 +153,13 @@ __device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // 16 consecutive columns of this thread's tensor-memory lane. The load is
@@ -407,7 +414,7 @@ __device__ __forceinline__ bool mend_v(uint32_t sv, int first, int end, bool zer
     return found;
 }
 
-// A weight pair, rounded to the operand type, and what it adds to the normaliser.
+// A weight pair, rounded to the operand type.
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float p0, float p1) { return F16 ? pack_f16(p0, p1) : pack_bf16(p0, p1); }
 
@@ -445,7 +452,7 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
             if (MODE == 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->k_full[g % L::kNK], (g / L::kNK) & 1)))
                 return false;
             const float *ks = reinterpret_cast<const float *>(sm + L::kKs) + (g % L::kNK) * kBN;
-            float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
             for (int c = col0; c < col0 + cols; c += W) {
                 float x[W];
@@ -492,8 +499,8 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                     if (grow) {
                         m = mx;
                         l *= alpha;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) l4[k] *= alpha;
+                        l2[0] = __fmul2_rn(l2[0], make_float2(alpha, alpha));
+                        l2[1] = __fmul2_rn(l2[1], make_float2(alpha, alpha));
                     }
 #pragma unroll 1
                     for (int e = col0; e < c; e += 16) {  // this tile's weights
@@ -526,16 +533,16 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                     uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float2 y = __fadd2_rn(make_float2(x[16 * h + 2 * i], x[16 * h + 2 * i + 1]),
+                        float2 y = __fadd2_rn(make_float2(x[16 * h + 2 * i], x[16 * h + 2 * i + 1]),
                                                     make_float2(ref, ref));
-                        w[i] = pack_p<kF16>(fast_exp2(y.x), fast_exp2(y.y));
-                        l4[i & 3] = kF16 ? fma_f16x2_acc(w[i], 0x3C003C00u, l4[i & 3])
-                                         : fma_bf16x2_acc(w[i], 0x3F803F80u, l4[i & 3]);
+                        y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                        w[i] = pack_p<kF16>(y.x, y.y);
+                        l2[i & 1] = __fadd2_rn(l2[i & 1], y);
                     }
                     tmem_st8(ts + c / 2 + 8 * h, w);
                 }
             }
-            l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
             if (cols < kBN) {  // the other copies' keys
                 const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 for (int c = cols / 2; c < kBN / 2; c += 8) tmem_st8(ts + ((col0 / 2 + c) & 31), zero);
@@ -961,67 +968,80 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
         __syncwarp();
     } else if (warp == L::kMmaWarp) {
         // ================================================ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = kFp8 ? idesc_f16(kRows, kBN, false) : idesc_bf16(kRows, kBN, false);
-            constexpr uint32_t kIdescPV = MODE == 1 ? idesc_f16(kRows, D, true) : idesc_bf16(kRows, D, true);
-            auto issue_s = [&](uint32_t t) -> bool {
-                if (!mbar_wait(&bars->k_full[t % kNK], (t / kNK) & 1)) return false;
-                tc_fence_after();
-                const uint32_t sk = base + L::kK + (t % kNK) * L::kKSlot;
-#pragma unroll 1
+        // The whole warp walks and waits, one elected lane issues: operands that
+        // are the same in every lane stay in uniform registers, which the MMA
+        // takes them from (from one lane alone, moving them there took longer
+        // than the products).
+        constexpr uint32_t kIdescS = kFp8 ? idesc_f16(kRows, kBN, false) : idesc_bf16(kRows, kBN, false);
+        constexpr uint32_t kIdescPV = MODE == 1 ? idesc_f16(kRows, D, true) : idesc_bf16(kRows, D, true);
+        const bool leader = elect_one();
+        auto wait_all = [](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+        };
+        const uint64_t dq = kFp8 ? desc8<D>(base + L::kQ) : sw128_desc(base + L::kQ, 16, 1024);
+        const uint64_t dk = kFp8 ? desc8<D>(base + L::kK) : sw128_desc(base + L::kK, 16, 1024);
+        const uint64_t dv = sw128_desc(base + L::kV, kBN * 128, 1024);
+        // descriptors count 16-byte units; the shared-memory window is below their 14 bits' 256 KB
+        auto issue_s = [&](uint32_t t) -> bool {
+            const uint32_t slot = t % kNK;
+            if (!wait_all(&bars->k_full[slot], (t / kNK) & 1)) return false;
+            tc_fence_after();
+            const uint64_t dks = dk + slot * (L::kKSlot >> 4);
+            if (leader) {
+#pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    const uint32_t sq = base + L::kQ + x * L::kQTile;
+                    const uint64_t dqx = dq + x * (L::kQTile >> 4);
                     const uint32_t ts = tmem + x * 256 + (t & 1) * kBN;
                     if constexpr (kFp8) {  // E4M3: format code 0 for A and B, 32 elements per step; hi, then lo
 #pragma unroll
-                        for (int kk = 0; kk < 2 * (D / 32); ++kk) {
-                            const uint32_t off = static_cast<uint32_t>((kk % (D / 32)) * 32);
-                            mma_f8(ts, desc8<D>(sq + (kk / (D / 32)) * kRows * D + off), desc8<D>(sk + off), kIdescS,
-                                   kk > 0 ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < 2 * (D / 32); ++kk)
+                            mma_f8(ts, dqx + (kk / (D / 32)) * (kRows * D >> 4) + (kk % (D / 32)) * 2,
+                                   dks + (kk % (D / 32)) * 2, kIdescS, kk > 0 ? 1u : 0u);
                     } else {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t ao = static_cast<uint32_t>((kk >> 2) * kRows * 128 + (kk & 3) * 32);
-                            const uint32_t bo = static_cast<uint32_t>((kk >> 2) * kBN * 128 + (kk & 3) * 32);
-                            mma_bf16(ts, sw128_desc(sq + ao, 16, 1024), sw128_desc(sk + bo, 16, 1024), kIdescS,
-                                     kk > 0 ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_bf16(ts, dqx + (kk >> 2) * (kRows * 128 >> 4) + (kk & 3) * 2,
+                                     dks + (kk >> 2) * (kBN * 128 >> 4) + (kk & 3) * 2, kIdescS, kk > 0 ? 1u : 0u);
                     }
-                    if (x == NT - 1) mma_commit(&bars->k_empty[t % kNK]);
+                    if (x == NT - 1) mma_commit(&bars->k_empty[slot]);
                     mma_commit(&bars->s_full[x][t & 1]);
                 }
-                return true;
-            };
-            bool ok = true;
-            for (int unit = 0; ok && walk.next(a, log2_g, u); ++unit) {
-                ok = mbar_wait(&bars->q_full, unit & 1) && issue_s(g);
-                for (int j = 0; ok && j < u.tiles; ++j) {
-                    const uint32_t t = g + j;
-                    // the next tile's S buffer was P of tile j - 1, which P V(j - 1) read before
-                    if (j + 1 < u.tiles) ok = issue_s(t + 1);
-                    ok = ok && mbar_wait(&bars->v_full[t % kNV], (t / kNV) & 1);
-                    // every softmax warp mends a part of the V of a tile with drafts
-                    if (NT > 1 && ok && u.t0 + (j + 1) * kBN > u.base)
-                        for (int x = 1; x < NT && ok; ++x) ok = mbar_wait(&bars->p_full[x][t & 1], (t >> 1) & 1);
-                    const uint32_t sv = base + L::kV + (t % kNV) * L::kVSlot;
-#pragma unroll 1
-                    for (int x = 0; x < NT && ok; ++x) {
-                        ok = mbar_wait(&bars->p_full[x][t & 1], (t >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = true;
+        for (int unit = 0; ok && walk.next(a, log2_g, u); ++unit) {
+            ok = wait_all(&bars->q_full, unit & 1) && issue_s(g);
+            for (int j = 0; ok && j < u.tiles; ++j) {
+                const uint32_t t = g + j, slot = t % kNV;
+                // the next tile's S buffer was P of tile j - 1, which P V(j - 1) read before
+                if (j + 1 < u.tiles) ok = issue_s(t + 1);
+                ok = ok && wait_all(&bars->v_full[slot], (t / kNV) & 1);
+                // every softmax warp mends a part of the V of a tile with drafts
+                if (NT > 1 && ok && u.t0 + (j + 1) * kBN > u.base)
+                    for (int x = 1; x < NT && ok; ++x) ok = wait_all(&bars->p_full[x][t & 1], (t >> 1) & 1);
+                const uint64_t dvs = dv + slot * (L::kVSlot >> 4);
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    ok = ok && wait_all(&bars->p_full[x][t & 1], (t >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
                             mma_bf16_ts(tmem + x * 256 + 128, tmem + x * 256 + (t & 1) * kBN + kk * 8,
-                                        sw128_desc(sv + static_cast<uint32_t>(kk * 16 * 128), kBN * 128, 1024),
-                                        kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
-                        if (x == NT - 1) mma_commit(&bars->v_empty[t % kNV]);
+                                        dvs + kk * (16 * 128 >> 4), kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (x == NT - 1) mma_commit(&bars->v_empty[slot]);
                         mma_commit(&bars->pv_done[x]);
                         if (j + 1 == u.tiles) mma_commit(&bars->o_done[x]);
                     }
+                    __syncwarp();
                 }
-                g += u.tiles;
             }
+            g += u.tiles;
+        }
+        if (leader) {
             if (!ok) set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
             // every MMA issued so far has finished before tensor memory is freed
             mma_commit(&bars->drained);

@@ -1102,22 +1102,25 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
 
     tc_fence_before();
     __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == L::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
     }
 }
 
-// Join of the cut units: block i looks at the border between the shares i and
-// i + 1; if it cuts a unit, the block makes its part of that unit's results
-// (the borders inside one unit divide its results among them).
+// Join of the cut units: the blocks (i, *) look at the border between the shares
+// i and i + 1; if it cuts a unit, they make its part of that unit's results (the
+// borders inside one unit divide its results among them). It may start before
+// the attention kernel has ended, and waits for that once it knows its part.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinSplit = 8;  // blocks per border: one block took 38 us for the results of 128 rows at a time
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int log2_g) {
     __shared__ long long scratch[16];
     const int tid = threadIdx.x, G = 1 << log2_g;
-    const int border = blockIdx.x + 1;
+    const int border = blockIdx.x / kJoinSplit + 1;
     int s;
     long long p;
     const Shares sh = find_share<kJoinThreads>(a, log2_g, border, scratch, s, p);
@@ -1131,35 +1134,34 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     int first = border - 1, end = border + 1;  // the shares that hold a piece
     while (tiles_before(sh.begin(first), p, q.tiles) > 0) --first;
     while (end < sh.shares && tiles_before(sh.begin(end), p, q.tiles) < q.tiles) ++end;
-    const int pieces = end - first, part = border - 1 - first, parts = pieces - 1;
+    const int pieces = end - first;
+    const int part = (border - 1 - first) * kJoinSplit + blockIdx.x % kJoinSplit, parts = (pieces - 1) * kJoinSplit;
     const int kh = k / q.row_tiles, row0 = (k % q.row_tiles) * a.unit_rows;
     const int rows = min(a.unit_rows, (q.c << log2_g) - row0);
-    const long long slot_rows = a.slot_rows;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
     // a unit's first piece is in its share's second slot, the others in the first ones
-    auto slot = [&](int i) { return i == 0 ? 2LL * first + 1 : 2LL * (first + i); };
+    auto slot = [&](int i) { return static_cast<long long>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * a.slot_rows; };
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = part * kJoinThreads + tid; i < rows * (D / 4); i += parts * kJoinThreads) {
         const int r = i / (D / 4), col = (i % (D / 4)) * 4;
-        float top = -INFINITY;
-        bool bad = false;
-        for (int n = 0; n < pieces; ++n) {
-            const float2 y = __ldg(ml + slot(n) * slot_rows + r);
-            top = fmaxf(top, y.x);
-            bad |= y.y < 0.0f;
-        }
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
+        float top = -INFINITY, sum = 0.0f;
         float4 acc = make_float4(0, 0, 0, 0);
+        bool bad = false;
+#pragma unroll 2
         for (int n = 0; n < pieces; ++n) {
-            const float2 y = __ldg(ml + slot(n) * slot_rows + r);
+            const long long at = slot(n) + r;
+            const float2 y = __ldcg(ml + at);
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D + col));
+            bad |= y.y < 0.0f;
             if (y.y == 0.0f) continue;  // a piece that the row saw nothing of
-            const float w = fast_exp2(y.x - ref) * y.y;
-            const float4 o = __ldg(reinterpret_cast<const float4 *>(a.part_o + (slot(n) * slot_rows + r) * D + col));
-            sum += w;
-            acc.x = fmaf(w, o.x, acc.x);
-            acc.y = fmaf(w, o.y, acc.y);
-            acc.z = fmaf(w, o.z, acc.z);
-            acc.w = fmaf(w, o.w, acc.w);
+            const float next = fmaxf(top, y.x), ref = next == -INFINITY ? 0.0f : next;
+            const float f = fast_exp2(top - ref), w = fast_exp2(y.x - ref) * y.y;  // f is 0 from top = -inf
+            top = next;
+            sum = fmaf(sum, f, w);
+            acc.x = fmaf(w, o.x, acc.x * f);
+            acc.y = fmaf(w, o.y, acc.y * f);
+            acc.z = fmaf(w, o.z, acc.z * f);
+            acc.w = fmaf(w, o.w, acc.w * f);
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const int row = row0 + r;
@@ -1216,8 +1218,16 @@ cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
     kern<<<a.max_shares, L::kThreads, L::kAlloc, stream>>>(a, log2_bs, log2_g, mk, mv);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.max_shares == 1) return e;
-    tree_join_kernel<D><<<a.max_shares - 1, kJoinThreads, 0, stream>>>(a, log2_g);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.max_shares - 1) * kJoinSplit);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, a, log2_g);
 }
 
 }  // namespace

@@ -98,54 +98,96 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(CompactArgs p) {
 // --------------------------------------------------------------------- load
 //
 // Output row cu_rows[i] + r is token starts[i] + r of sequence i: bf16 rows
-// copied, E4M3 codes times their scale in binary32 and rounded to bf16. One
-// thread makes 8 elements of a K and of a V row; a row's sequence is found by
-// bisection over cu_rows.
+// copied, E4M3 codes times their scale in binary32 and rounded to bf16.
+// Bandwidth bounds it. A warp takes up to kLoadRows consecutive rows: its lanes find
+// each row's sequence (by bisection over cu_rows) and pool block together, one
+// row per lane, and then move the rows' 16-byte output chunks, kLoadBatch of a
+// lane in flight.
+constexpr int kLoadThreads = 256;
+constexpr int kLoadRows = 8;  // at most; fewer while that leaves SMs without warps
+constexpr int kLoadBatch = 4;
+
+// Output chunk of 8 elements from a pool row's chunk.
 template <int MODE>
-__global__ void __launch_bounds__(256) load_kernel(LoadArgs p) {
-    const int cpr = p.head_dim / 8;
-    const long long units = (long long)p.total_rows * p.num_kv_heads * cpr;
-    const long long stride = (long long)gridDim.x * blockDim.x;
+__device__ __forceinline__ uint4 load_chunk(const void *pool, long long at) {
+    if constexpr (MODE == 0) return __ldg(static_cast<const uint4 *>(pool) + at);
+    const uint2 w = __ldg(static_cast<const uint2 *>(pool) + at);
+    return make_uint4(w.x, w.y, 0, 0);
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kLoadThreads) load_kernel(LoadArgs p, int rows) {
+    const int cpr = p.head_dim / 8, per_row = p.num_kv_heads * cpr;
+    const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0) {  // the bisection below trusts an ascending list
-        for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x)
+        for (int i = threadIdx.x; i < p.num_seqs; i += kLoadThreads)
             if (p.cu_rows[i] < 0 || p.cu_rows[i + 1] < p.cu_rows[i] || p.cu_rows[i + 1] > p.total_rows)
                 set_error(p.dev_err, PKV_DEVERR_BOUNDS);
     }
-    for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += stride) {
-        const int c = (int)(u % cpr);
-        const long long rh = u / cpr;  // output row * num_kv_heads + head
-        const int kh = (int)(rh % p.num_kv_heads);
-        const int row = (int)(rh / p.num_kv_heads);
-        int lo = 0, hi = p.num_seqs;  // the last sequence that starts at or before the row
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (__ldg(p.cu_rows + mid) <= row) lo = mid;
-            else hi = mid;
-        }
-        const int first = __ldg(p.cu_rows + lo);
-        if (row < first || row >= __ldg(p.cu_rows + lo + 1)) continue;  // no sequence's row: left as it is
-        const long long t = (p.starts ? (long long)__ldg(p.starts + lo) : 0) + (row - first);
-        uint4 k = make_uint4(0, 0, 0, 0), v = k;
-        int blk = -1;
-        if (t >= 0 && t < (long long)p.max_blocks_per_seq * p.block_size)
-            blk = __ldg(p.block_tables + (long long)lo * p.max_blocks_per_seq + t / p.block_size);
-        if (blk < 0 || blk >= p.num_blocks) {
-            set_error(p.dev_err, PKV_DEVERR_BOUNDS);
-        } else {
-            const long long prow = ((long long)blk * p.num_kv_heads + kh) * p.block_size + t % p.block_size;
-            if constexpr (MODE == 0) {
-                k = __ldg(static_cast<const uint4 *>(p.k_cache) + prow * cpr + c);
-                v = __ldg(static_cast<const uint4 *>(p.v_cache) + prow * cpr + c);
-            } else {
-                const long long sidx = MODE == 2 ? prow : kh;
-                k = e4m3x8_scaled_bf16x8(__ldg(static_cast<const uint2 *>(p.k_cache) + prow * cpr + c),
-                                         __ldg(p.k_scale + sidx));
-                v = e4m3x8_scaled_bf16x8(__ldg(static_cast<const uint2 *>(p.v_cache) + prow * cpr + c),
-                                         __ldg(p.v_scale + sidx));
+    const long long tiles = ((long long)p.total_rows + rows - 1) / rows;
+    const long long warps = (long long)gridDim.x * (kLoadThreads / 32);
+    for (long long tile = (long long)blockIdx.x * (kLoadThreads / 32) + (threadIdx.x >> 5); tile < tiles; tile += warps) {
+        const long long row0 = tile * rows;
+        // lane r: row row0 + r; base: pool row of its KV head 0, -1: zeros, -2: no sequence's row
+        long long base = -2;
+        if (lane < rows && row0 + lane < p.total_rows) {
+            const int row = (int)(row0 + lane);
+            int lo = 0, hi = p.num_seqs;  // the last sequence that starts at or before the row
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (__ldg(p.cu_rows + mid) <= row) lo = mid;
+                else hi = mid;
+            }
+            const int first = __ldg(p.cu_rows + lo);
+            if (row >= first && row < __ldg(p.cu_rows + lo + 1)) {
+                const long long t = (p.starts ? (long long)__ldg(p.starts + lo) : 0) + (row - first);
+                int blk = -1;
+                if (t >= 0 && t < (long long)p.max_blocks_per_seq * p.block_size)
+                    blk = __ldg(p.block_tables + (long long)lo * p.max_blocks_per_seq + t / p.block_size);
+                if (blk < 0 || blk >= p.num_blocks) {
+                    set_error(p.dev_err, PKV_DEVERR_BOUNDS);
+                    base = -1;
+                } else {
+                    base = (long long)blk * p.num_kv_heads * p.block_size + t % p.block_size;
+                }
             }
         }
-        p.k_out[u] = k;
-        p.v_out[u] = v;
+        const int units = rows * per_row;
+        for (int i0 = 0; i0 < units; i0 += 32 * kLoadBatch) {
+            uint4 k[kLoadBatch], v[kLoadBatch];
+            float ks[kLoadBatch], vs[kLoadBatch];
+            long long from[kLoadBatch];
+#pragma unroll
+            for (int j = 0; j < kLoadBatch; ++j) {
+                const int i = i0 + 32 * j + lane;
+                const int r = i / per_row, x = i - r * per_row;
+                const int kh = x / cpr, c = x - kh * cpr;
+                const long long b = __shfl_sync(0xffffffffu, base, r & 31);
+                from[j] = i < units ? b : -2;
+                k[j] = v[j] = make_uint4(0, 0, 0, 0);
+                ks[j] = vs[j] = 0.0f;
+                if (from[j] >= 0) {
+                    const long long prow = b + (long long)kh * p.block_size;
+                    k[j] = load_chunk<MODE>(p.k_cache, prow * cpr + c);
+                    v[j] = load_chunk<MODE>(p.v_cache, prow * cpr + c);
+                    if constexpr (MODE != 0) {
+                        ks[j] = __ldg(p.k_scale + (MODE == 2 ? prow : kh));
+                        vs[j] = __ldg(p.v_scale + (MODE == 2 ? prow : kh));
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kLoadBatch; ++j) {
+                if (from[j] == -2) continue;
+                if constexpr (MODE != 0) {
+                    k[j] = e4m3x8_scaled_bf16x8(make_uint2(k[j].x, k[j].y), ks[j]);
+                    v[j] = e4m3x8_scaled_bf16x8(make_uint2(v[j].x, v[j].y), vs[j]);
+                }
+                const long long to = row0 * per_row + i0 + 32 * j + lane;
+                __stcs(p.k_out + to, k[j]);  // not read again here
+                __stcs(p.v_out + to, v[j]);
+            }
+        }
     }
 }
 
@@ -162,16 +204,18 @@ cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_load(const LoadArgs &a, int mode, int num_sms, cudaStream_t stream) {
-    const long long units = (long long)a.total_rows * a.num_kv_heads * (a.head_dim / 8);
-    long long blocks = (units + 255) / 256;
-    const long long cap = (long long)num_sms * 16;
+    long long rows = a.total_rows / (32LL * num_sms);  // rows per warp
+    rows = rows < 1 ? 1 : rows > kLoadRows ? kLoadRows : rows;
+    const long long warps = (a.total_rows + rows - 1) / rows;
+    long long blocks = (warps + kLoadThreads / 32 - 1) / (kLoadThreads / 32);
+    const long long cap = (long long)num_sms * 8;
     if (blocks > cap) blocks = cap;
     if (mode == 2)
-        load_kernel<2><<<(unsigned)blocks, 256, 0, stream>>>(a);
+        load_kernel<2><<<(unsigned)blocks, kLoadThreads, 0, stream>>>(a, (int)rows);
     else if (mode == 1)
-        load_kernel<1><<<(unsigned)blocks, 256, 0, stream>>>(a);
+        load_kernel<1><<<(unsigned)blocks, kLoadThreads, 0, stream>>>(a, (int)rows);
     else
-        load_kernel<0><<<(unsigned)blocks, 256, 0, stream>>>(a);
+        load_kernel<0><<<(unsigned)blocks, kLoadThreads, 0, stream>>>(a, (int)rows);
     return cudaGetLastError();
 }
 

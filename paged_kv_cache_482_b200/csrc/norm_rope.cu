@@ -16,8 +16,13 @@
 // contiguous, tokens lie a caller-given stride apart (for instance one row of
 // the fused QKV projection).
 //
-// One thread handles 8 pairs of one (token, row); a row takes head_dim / 16
-// adjacent lanes, which add up the row's sum of squares with shuffles.
+// Bandwidth bounds it (4 bytes of q per element, 2 of k and v and what the cache
+// holds), if the table's row, twice the size of a q row, is not read again for
+// every head. So a warp takes a token: its lanes hold the token's cosines and
+// sines and the weight in registers, and walk the token's heads, 32 / L at a
+// time (a row of head_dim elements is L = head_dim / 16 lanes of 8 pairs, which
+// add up its sum of squares with shuffles), kBatch steps' loads in flight.
+// Few tokens are spread over more warps, each with a part of the heads.
 #include "pkv_common.cuh"
 #include "pkv_launch.h"
 #include "store_common.cuh"
@@ -45,169 +50,270 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// E4M3 of x / scale (one IEEE division each, round to nearest even, saturating).
+// E4M3 of x / scale, as with one IEEE division each, round to nearest even,
+// saturating. The quotient is formed with one reciprocal: y = x * (1 / scale) is
+// within 3 units of its last place of the division's result, so both round to
+// the same code unless a point between two codes is that near. Those points, and
+// the codes, have 19 zeros at the end of their binary32 significand: where y's
+// last 19 bits are within 3 of zero the divisions are done (not below 2^-11 or
+// above 440, where both round to 0 or 448).
 __device__ __forceinline__ uint2 quantise8f(const float (&x)[8], float scale) {
-    uint32_t out[2] = {0u, 0u};
+    const bool plain = scale > 1e-36f && scale < 1e36f;  // the reciprocal is a normal number
+    const float r = plain ? __frcp_rn(scale) : 0.0f;
+    float y[8];
+    bool near = !plain;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t c = __nv_cvt_float_to_fp8(__fdiv_rn(x[j], scale), __NV_SATFINITE, __NV_E4M3);
-        out[j >> 2] |= c << ((j & 3) * 8);
+        y[j] = x[j] * r;
+        near |= ((__float_as_uint(y[j]) + 3u) & 0x7FFFFu) <= 6u && fabsf(y[j]) > 4e-4f && fabsf(y[j]) < 440.0f;
     }
-    return make_uint2(out[0], out[1]);
+    if (near) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(x[j], scale);
+    }
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        out[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * j], y[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(out[0] | (out[1] << 16), out[2] | (out[3] << 16));
+}
+
+constexpr int kThreads = 128;
+constexpr int kBatch = 2;
+// Resident blocks per SM (102 registers a thread): with 4 and 6, 8192 tokens took
+// 47.5 and 48.1 us instead of 43.1, 2777 into an E4M3 cache 18.3 and 22.5 instead of 16.
+constexpr int kMinBlocks = 5;
+
+__device__ __forceinline__ uint4 load_row(const __nv_bfloat16 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Sum or maximum over the L adjacent lanes of a row (every lane of the warp calls).
+__device__ __forceinline__ float row_sum(float x, int L) {
+    for (int o = L >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ __forceinline__ float row_max(float x, int L) {
+    for (int o = L >> 1; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// 8 pairs of a row: x (first elements) and y (second ones) normed and rotated.
+template <int STYLE>
+__device__ __forceinline__ void norm_rotate(uint4 a, uint4 b, const uint4 &wa, const uint4 &wb, const float (&cs)[8],
+                                            const float (&sn)[8], int L, float inv_d, float eps, float (&x)[8],
+                                            float (&y)[8]) {
+    if constexpr (STYLE == 1) {
+        uint4 t0, t1;
+        deinterleave(a, b, t0, t1);
+        a = t0;
+        b = t1;
+    }
+    unpack8(a, x);
+    unpack8(b, y);
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+    const float inv = rsqrtf(fmaf(row_sum(ss, L), inv_d, eps));
+    float u[8], v[8];
+    unpack8(wa, u);
+    unpack8(wb, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float na = x[j] * inv * u[j], nb = y[j] * inv * v[j];
+        x[j] = fmaf(-nb, sn[j], na * cs[j]);
+        y[j] = fmaf(na, sn[j], nb * cs[j]);
+    }
+}
+
+// The two 16-byte chunks of a bf16 row.
+template <int STYLE>
+__device__ __forceinline__ void pack_row(const float (&x)[8], const float (&y)[8], uint4 &a, uint4 &b) {
+    a = pack8(x);
+    b = pack8(y);
+    if constexpr (STYLE == 1) {
+        uint4 t0, t1;
+        interleave(a, b, t0, t1);
+        a = t0;
+        b = t1;
+    }
 }
 
 // MODE 0: bf16 cache; 1: E4M3, a scale per KV head; 2: E4M3, a scale per row.
+// A token's rows are `steps` steps of 32 / L rows: the q heads', the k heads',
+// the v heads'. A warp takes up to `part` of them at a time; the loads of the
+// next kBatch steps are issued before the current ones are worked on, and the
+// first ones before the token's position and slot are known.
 template <int MODE, int STYLE>
-__global__ void __launch_bounds__(256) store_norm_rope_kernel(NormRopeArgs p) {
-    const int L = p.head_dim / 16;  // lanes per row
-    const int rows = p.num_q_heads + p.num_kv_heads;
-    const long long units = (long long)p.num_tokens * rows * L;
-    const long long stride = (long long)gridDim.x * blockDim.x;
-    for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += stride) {
-        const int c = (int)(u % L);
-        const long long rowi = u / L;
-        const int r = (int)(rowi % rows);
-        const long long token = rowi / rows;
-        // 16-byte chunks of the two halves this lane handles
-        const int ca = STYLE == 1 ? 2 * c : c;
-        const int cb = STYLE == 1 ? 2 * c + 1 : c + L;
-        const bool is_q = r < p.num_q_heads;
-        const int head = is_q ? r : r - p.num_q_heads;
-        const int m = __ldg(p.positions + token);
-        if (m < 0 || m >= p.max_position) {
-            if (c == 0 && r == 0) set_error(p.dev_err, PKV_DEVERR_BOUNDS);
-            continue;
-        }
-        long long slot = 0;
-        if (!is_q) {
-            slot = __ldg(p.slots + token);
-            if (slot < 0) continue;
-            if (slot >= p.pool_slots) {
-                set_error(p.dev_err, PKV_DEVERR_BOUNDS);
-                continue;
-            }
-        }
-        const __nv_bfloat16 *src = is_q ? p.q + token * p.q_stride : p.k + token * p.k_stride;
-        const uint4 *x = reinterpret_cast<const uint4 *>(src + (long long)head * p.head_dim);
-        uint4 a = x[ca], b = x[cb];
-        const uint4 *w = reinterpret_cast<const uint4 *>(is_q ? p.q_weight : p.k_weight);
-        uint4 wa = __ldg(w + ca), wb = __ldg(w + cb);
+__global__ void __launch_bounds__(kThreads, kMinBlocks) store_norm_rope_kernel(NormRopeArgs p, int log2_l, int part,
+                                                                               int parts) {
+    const int L = 1 << log2_l, lane = threadIdx.x & 31;
+    const int c = lane & (L - 1), sub = lane >> log2_l, rows = 32 >> log2_l;
+    const int q_steps = (p.num_q_heads + rows - 1) / rows, kv_steps = (p.num_kv_heads + rows - 1) / rows;
+    const int k_end = q_steps + kv_steps, steps = k_end + kv_steps;
+    // element offsets of the two halves this lane handles, in a row
+    const int ea = 8 * (STYLE == 1 ? 2 * c : c), eb = 8 * (STYLE == 1 ? 2 * c + 1 : c + L);
+    const float inv_d = 1.0f / (float)p.head_dim;  // exact: a power of two
+    auto load_weight = [&](const __nv_bfloat16 *w, uint4 &wa, uint4 &wb) {
+        wa = __ldg(reinterpret_cast<const uint4 *>(w + ea));
+        wb = __ldg(reinterpret_cast<const uint4 *>(w + eb));
         if constexpr (STYLE == 1) {
             uint4 t0, t1;
-            deinterleave(a, b, t0, t1);
-            a = t0;
-            b = t1;
             deinterleave(wa, wb, t0, t1);
             wa = t0;
             wb = t1;
         }
-        float xa[8], xb[8], va[8], vb[8];
-        unpack8(a, xa);
-        unpack8(b, xb);
-        unpack8(wa, va);
-        unpack8(wb, vb);
-        float ss = 0.f;
+    };
+    const long long units = (long long)p.num_tokens * parts;
+    const long long warps = (long long)gridDim.x * (kThreads / 32);
+    for (long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+        const long long token = u / parts;
+        const int s0 = (int)(u % parts) * part, s1 = min(s0 + part, steps);
+        const int m = __ldg(p.positions + token);
+        const long long slot = __ldg(p.slots + token);
+        const __nv_bfloat16 *qt = p.q + token * p.q_stride, *kt = p.k + token * p.k_stride, *vt = p.v + token * p.v_stride;
+        uint4 na[kBatch], nb[kBatch];  // the next steps' chunks
+        auto load = [&](int s) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
-        const int lane = threadIdx.x & 31;
-        const unsigned group = (L == 32 ? 0xffffffffu : ((1u << L) - 1u)) << (lane & ~(L - 1));
-        for (int o = L >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o, L);
-        const float inv = rsqrtf(ss / (float)p.head_dim + p.eps);
-        const float *cs = p.cos_sin + (long long)m * p.head_dim + 8 * c;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float cc = __ldg(cs + j), sn = __ldg(cs + p.head_dim / 2 + j);
-            const float na = xa[j] * inv * va[j], nb = xb[j] * inv * vb[j];
-            xa[j] = fmaf(-nb, sn, na * cc);
-            xb[j] = fmaf(na, sn, nb * cc);
-        }
-        if (is_q || MODE == 0) {
-            uint4 oa = pack8(xa), ob = pack8(xb);
-            if constexpr (STYLE == 1) {
-                uint4 t0, t1;
-                interleave(oa, ob, t0, t1);
-                oa = t0;
-                ob = t1;
-            }
-            if (is_q) {
-                uint4 *dst = reinterpret_cast<uint4 *>(p.q_out + token * p.q_out_stride + (long long)head * p.head_dim);
-                dst[ca] = oa;
-                dst[cb] = ob;
-                continue;
-            }
-            a = oa;
-            b = ob;
-        }
-        const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v + token * p.v_stride + (long long)head * p.head_dim);
-        const uint4 v0 = vsrc[ca], v1 = vsrc[cb];
-        const long long blk = slot / p.block_size;
-        const long long off = slot - blk * p.block_size;
-        const long long row = (blk * p.num_kv_heads + head) * p.block_size + off;  // pool row
-        const long long ea = row * p.head_dim + ca * 8LL, eb = row * p.head_dim + cb * 8LL;
-        if constexpr (MODE == 0) {
-            __nv_bfloat16 *kc = static_cast<__nv_bfloat16 *>(p.k_cache), *vc = static_cast<__nv_bfloat16 *>(p.v_cache);
-            *reinterpret_cast<uint4 *>(kc + ea) = a;
-            *reinterpret_cast<uint4 *>(kc + eb) = b;
-            *reinterpret_cast<uint4 *>(vc + ea) = v0;
-            *reinterpret_cast<uint4 *>(vc + eb) = v1;
-        } else {
-            float ks, vs;
-            if constexpr (MODE == 2) {
-                float km = 0.f, vm = fmaxf(amax8(v0), amax8(v1));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) km = fmaxf(km, fmaxf(fabsf(xa[j]), fabsf(xb[j])));
-                for (int o = L >> 1; o > 0; o >>= 1) {
-                    km = fmaxf(km, __shfl_xor_sync(group, km, o, L));
-                    vm = fmaxf(vm, __shfl_xor_sync(group, vm, o, L));
+            for (int i = 0; i < kBatch; ++i) {
+                const int si = s + i;
+                const int head = (si < q_steps ? si : si < k_end ? si - q_steps : si - k_end) * rows + sub;
+                const __nv_bfloat16 *src = (si < q_steps ? qt : si < k_end ? kt : vt) + (long long)head * p.head_dim;
+                na[i] = nb[i] = make_uint4(0, 0, 0, 0);
+                if (si < s1 && head < (si < q_steps ? p.num_q_heads : p.num_kv_heads)) {
+                    na[i] = load_row(src + ea);
+                    nb[i] = load_row(src + eb);
                 }
-                ks = token_scale(km);
-                vs = token_scale(vm);
-                if (c == 0) {
-                    p.k_scale[row] = ks;
-                    p.v_scale[row] = vs;
+            }
+        };
+        load(s0);
+        if (m < 0 || m >= p.max_position) {  // the same for the whole warp
+            if (lane == 0 && s0 == 0) set_error(p.dev_err, PKV_DEVERR_BOUNDS);
+            continue;
+        }
+        int last = s1;  // steps to be done
+        if (slot < 0 || slot >= p.pool_slots) {
+            last = min(s1, q_steps);
+            if (slot >= 0 && s1 > q_steps && lane == 0) set_error(p.dev_err, PKV_DEVERR_BOUNDS);
+        }
+        const long long blk = slot / p.block_size, off = slot - blk * p.block_size;
+        float cs[8], sn[8];
+        const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (long long)m * p.head_dim + 8 * c);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 x = __ldg(row + h), y = __ldg(row + p.head_dim / 8 + h);
+            cs[4 * h] = x.x;
+            cs[4 * h + 1] = x.y;
+            cs[4 * h + 2] = x.z;
+            cs[4 * h + 3] = x.w;
+            sn[4 * h] = y.x;
+            sn[4 * h + 1] = y.y;
+            sn[4 * h + 2] = y.z;
+            sn[4 * h + 3] = y.w;
+        }
+        uint4 wa, wb;  // the q weight, then the k weight
+        load_weight(s0 < q_steps ? p.q_weight : p.k_weight, wa, wb);
+        for (int s = s0; s < last; s += kBatch) {
+            uint4 a[kBatch], b[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                a[i] = na[i];
+                b[i] = nb[i];
+            }
+            if (s + kBatch < last) load(s + kBatch);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int si = s + i;  // the same in every lane, so is the kind of row
+                if (si >= last) break;
+                if (si == q_steps && si > s0) load_weight(p.k_weight, wa, wb);
+                float x[8], y[8];
+                if (si < q_steps) {
+                    const int head = si * rows + sub;
+                    norm_rotate<STYLE>(a[i], b[i], wa, wb, cs, sn, L, inv_d, p.eps, x, y);
+                    if (head < p.num_q_heads) {
+                        uint4 oa, ob;
+                        pack_row<STYLE>(x, y, oa, ob);
+                        __nv_bfloat16 *dst = p.q_out + token * p.q_out_stride + (long long)head * p.head_dim;
+                        *reinterpret_cast<uint4 *>(dst + ea) = oa;
+                        *reinterpret_cast<uint4 *>(dst + eb) = ob;
+                    }
+                    continue;
                 }
-            } else {
-                ks = __ldg(p.k_scale + head);
-                vs = __ldg(p.v_scale + head);
+                const bool is_k = si < k_end;
+                const int head = (si - (is_k ? q_steps : k_end)) * rows + sub;
+                const bool live = head < p.num_kv_heads;
+                const long long prow = (blk * p.num_kv_heads + (live ? head : 0)) * p.block_size + off;  // pool row
+                uint4 oa = a[i], ob = b[i];
+                if (is_k) norm_rotate<STYLE>(a[i], b[i], wa, wb, cs, sn, L, inv_d, p.eps, x, y);
+                if constexpr (MODE == 0) {
+                    if (is_k) pack_row<STYLE>(x, y, oa, ob);
+                    if (live) {
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(is_k ? p.k_cache : p.v_cache) + prow * p.head_dim;
+                        *reinterpret_cast<uint4 *>(dst + ea) = oa;
+                        *reinterpret_cast<uint4 *>(dst + eb) = ob;
+                    }
+                } else {
+                    if (!is_k) {
+                        unpack8(oa, x);
+                        unpack8(ob, y);
+                    }
+                    float *scales = is_k ? p.k_scale : p.v_scale;
+                    float scale;
+                    if constexpr (MODE == 2) {
+                        float top = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
+                        scale = token_scale(row_max(top, L));
+                        if (live && c == 0) scales[prow] = scale;
+                    } else {
+                        scale = __ldg(scales + (live ? head : 0));
+                    }
+                    uint2 ca = quantise8f(x, scale), cb = quantise8f(y, scale);
+                    if (STYLE == 1 && is_k) {  // the codes back to interleaved order
+                        const uint2 t0 = ca, t1 = cb;
+                        ca = make_uint2(__byte_perm(t0.x, t1.x, 0x5140), __byte_perm(t0.x, t1.x, 0x7362));
+                        cb = make_uint2(__byte_perm(t0.y, t1.y, 0x5140), __byte_perm(t0.y, t1.y, 0x7362));
+                    }
+                    if (live) {
+                        uint8_t *dst = static_cast<uint8_t *>(is_k ? p.k_cache : p.v_cache) + prow * p.head_dim;
+                        *reinterpret_cast<uint2 *>(dst + ea) = ca;
+                        *reinterpret_cast<uint2 *>(dst + eb) = cb;
+                    }
+                }
             }
-            uint2 qa = quantise8f(xa, ks), qb = quantise8f(xb, ks);
-            if constexpr (STYLE == 1) {  // the codes back to interleaved order
-                const uint2 t0 = qa, t1 = qb;
-                qa = make_uint2(__byte_perm(t0.x, t1.x, 0x5140), __byte_perm(t0.x, t1.x, 0x7362));
-                qb = make_uint2(__byte_perm(t0.y, t1.y, 0x5140), __byte_perm(t0.y, t1.y, 0x7362));
-            }
-            uint8_t *kc = static_cast<uint8_t *>(p.k_cache), *vc = static_cast<uint8_t *>(p.v_cache);
-            *reinterpret_cast<uint2 *>(kc + ea) = qa;
-            *reinterpret_cast<uint2 *>(kc + eb) = qb;
-            *reinterpret_cast<uint2 *>(vc + ea) = quantise8(v0, vs);
-            *reinterpret_cast<uint2 *>(vc + eb) = quantise8(v1, vs);
         }
     }
 }
 
-template <int MODE>
-void launch_mode(const NormRopeArgs &p, int style, unsigned blocks, cudaStream_t stream) {
-    if (style == 1)
-        store_norm_rope_kernel<MODE, 1><<<blocks, 256, 0, stream>>>(p);
-    else
-        store_norm_rope_kernel<MODE, 0><<<blocks, 256, 0, stream>>>(p);
+template <int MODE, int STYLE>
+cudaError_t launch_style(const NormRopeArgs &p, int num_sms, cudaStream_t stream) {
+    auto kern = store_norm_rope_kernel<MODE, STYLE>;
+    int log2_l = 0;
+    while ((16 << log2_l) < p.head_dim) ++log2_l;
+    const int rows = 32 >> log2_l;
+    const int steps = (p.num_q_heads + rows - 1) / rows + 2 * ((p.num_kv_heads + rows - 1) / rows);
+    // a token is divided among warps while that leaves resident ones without work
+    const long long resident = (long long)num_sms * kMinBlocks * (kThreads / 32);
+    long long part = ((long long)p.num_tokens * steps + resident - 1) / resident;
+    if (part > steps) part = steps;
+    const int parts = (int)((steps + part - 1) / part);
+    const long long units = (long long)p.num_tokens * parts;
+    long long blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > (long long)num_sms * kMinBlocks) blocks = (long long)num_sms * kMinBlocks;
+    kern<<<(unsigned)blocks, kThreads, 0, stream>>>(p, log2_l, (int)part, parts);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_store_norm_rope(const NormRopeArgs &a, int style, int mode, int num_sms, cudaStream_t stream) {
-    const long long units = (long long)a.num_tokens * (a.num_q_heads + a.num_kv_heads) * (a.head_dim / 16);
-    long long blocks = (units + 255) / 256;
-    const long long cap = (long long)num_sms * 16;
-    if (blocks > cap) blocks = cap;
-    if (blocks < 1) blocks = 1;
-    if (mode == 2)
-        launch_mode<2>(a, style, (unsigned)blocks, stream);
-    else if (mode == 1)
-        launch_mode<1>(a, style, (unsigned)blocks, stream);
-    else
-        launch_mode<0>(a, style, (unsigned)blocks, stream);
-    return cudaGetLastError();
+    if (mode == 2) return style == 1 ? launch_style<2, 1>(a, num_sms, stream) : launch_style<2, 0>(a, num_sms, stream);
+    if (mode == 1) return style == 1 ? launch_style<1, 1>(a, num_sms, stream) : launch_style<1, 0>(a, num_sms, stream);
+    return style == 1 ? launch_style<0, 1>(a, num_sms, stream) : launch_style<0, 0>(a, num_sms, stream);
 }
 
 }  // namespace pkv

@@ -175,69 +175,80 @@ def cache_dtype(k_cache: torch.Tensor, k_scale=None) -> int:
     return _cache_dtype(k_cache, k_scale)
 
 
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_E4M3 = torch.float8_e4m3fn
+
+
 def _pool_args(k_cache, v_cache, k_scale, v_scale) -> int:
     """Check a pool pair and its scales; returns the cache type."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    t, shape = k_cache.dtype, k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != t:
         raise ValueError("the pools must be two [num_blocks, num_kv_heads, block_size, head_dim] tensors of one type")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("the pools must be contiguous")
-    dt = _cache_dtype(k_cache, k_scale)
-    if dt != PKV_CACHE_BF16:
-        if k_scale is None or v_scale is None:
-            raise ValueError("an E4M3 cache needs k_scale and v_scale")
-        shape = k_cache.shape[1:2] if dt == PKV_CACHE_FP8_E4M3 else k_cache.shape[:3]
-        for t in (k_scale, v_scale):
-            if t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous():
-                raise ValueError("scales must be contiguous fp32 [num_kv_heads], or scale pools [num_blocks, "
-                                 "num_kv_heads, block_size], both of one kind")
-    return dt
+    if t == _BF16:
+        return PKV_CACHE_BF16
+    if t != _U8 and t != _E4M3:
+        raise TypeError(f"KV pool dtype {t}: expected bfloat16 or an 8-bit E4M3 container")
+    if k_scale is None or v_scale is None:
+        raise ValueError("an E4M3 cache needs k_scale and v_scale")
+    token = k_scale.dim() == 3
+    shape = shape[:3] if token else shape[1:2]
+    for s in (k_scale, v_scale):
+        if s.shape != shape or s.dtype != _F32 or not s.is_contiguous():
+            raise ValueError("scales must be contiguous fp32 [num_kv_heads], or scale pools [num_blocks, "
+                             "num_kv_heads, block_size], both of one kind")
+    return PKV_CACHE_FP8_E4M3_TOKEN if token else PKV_CACHE_FP8_E4M3
 
 
 def _i32(t, name, shape):
-    if t.dtype != torch.int32 or not t.is_contiguous():
+    if t.dtype != _I32 or not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous int32")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _on_device(*tensors) -> torch.device:
-    """The one CUDA device that holds every given tensor."""
-    dev = tensors[0].device
-    if dev.type != "cuda":
+def _on_device(*tensors) -> int:
+    """The index of the one CUDA device that holds every given tensor."""
+    index = tensors[0].get_device()  # -1 on the CPU
+    if index < 0:
         raise ValueError("the tensors must be on a CUDA device")
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError("the tensors must be on one CUDA device")
-    return dev
+    return index
 
 
-def _torch_stream(stream, dev):
-    """``stream`` (torch stream, raw handle or None: the device's current one) as a torch stream."""
-    if stream is None:
-        return torch.cuda.current_stream(dev)
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
+def _torch_stream(stream, index):
+    """``stream`` (a torch stream or a raw handle) as a torch stream of device ``index``."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=index)
 
 
-def _empty(shape, dtype, dev, stream):
+def _empty(shape, dtype, index, stream):
     """A new tensor whose memory belongs to ``stream``, where the kernels use it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(_torch_stream(stream, dev)):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=index)
+    with torch.cuda.stream(_torch_stream(stream, index)):
+        return torch.empty(shape, dtype=dtype, device=index)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _run(fn, where, dev, stream, *args):
-    """Call a launching entry point with ``dev`` current and the stream last."""
-    handle = _torch_stream(stream, dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, handle), where)
+def _run(fn, where, index, stream, *args):
+    """Call a launching entry point with device ``index`` current and the stream last."""
+    if stream is None:
+        handle = torch.cuda.current_stream(index).cuda_stream
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, handle), where)
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != PKV_OK:
+        raise PagedKVError(status, where)
 
 
 def _check(status: int, where: str):
@@ -298,16 +309,16 @@ def store_kvcache_rope(k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
     return q_out
 
 
-def _heads(t, name, N, d):
+def _heads(t, name, N, heads, d):
     """Token stride of a bf16 [N, heads, d] tensor whose heads are contiguous."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype != _BF16:
         raise TypeError(f"{name} must be bfloat16")
-    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != d:
-        raise ValueError(f"{name} must be [N, heads, head_dim]")
+    if t.shape != (N, heads, d):
+        raise ValueError(f"{name} must have shape {(N, heads, d)}, not {tuple(t.shape)}")
     sn, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and t.shape[1] > 1):
+    if (sd != 1 and d > 1) or (sh != d and heads > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return sn if N > 1 else t.shape[1] * d  # the stride of a single token is never used
+    return sn if N > 1 else heads * d  # the stride of a single token is never used
 
 
 def store_kvcache_norm_rope(k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, k_weight, eps, q=None,
@@ -321,39 +332,38 @@ def store_kvcache_norm_rope(k, v, k_cache, v_cache, slot_mapping, positions, cos
     dt = _pool_args(k_cache, v_cache, k_scale, v_scale)
     nblk, nkv, bs, d = k_cache.shape
     N = k.shape[0]
-    k_stride, v_stride = _heads(k, "k", N, d), _heads(v, "v", N, d)
-    if k.shape[1] != nkv or v.shape[1] != nkv:
-        raise ValueError("k and v must have the pools' KV heads")
+    k_stride, v_stride = _heads(k, "k", N, nkv, d), _heads(v, "v", N, nkv, d)
     _i32(slot_mapping, "slot_mapping", (N,))
     _i32(positions, "positions", (N,))
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    if cos_sin.dtype != _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise TypeError("cos_sin must be a contiguous fp32 [max_position, head_dim] table")
-    if cos_sin.shape[1] != d:
+    max_position, dc = cos_sin.shape
+    if dc != d:
         raise ValueError("cos_sin does not match head_dim")
+    if k_weight.dtype != _BF16 or k_weight.shape != (d,) or not k_weight.is_contiguous():
+        raise TypeError("the norm weights must be contiguous bfloat16 [head_dim]")
     nq = q_stride = out_stride = 0
     if q is not None:
-        q_stride = _heads(q, "q", N, d)
         nq = q.shape[1]
+        q_stride = _heads(q, "q", N, nq, d)
         if q_weight is None:
             raise ValueError("q needs q_weight")
+        if q_weight.dtype != _BF16 or q_weight.shape != (d,) or not q_weight.is_contiguous():
+            raise TypeError("the norm weights must be contiguous bfloat16 [head_dim]")
         if q_out is not None:
-            out_stride = _heads(q_out, "q_out", N, d)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must be shaped like q")
+            out_stride = _heads(q_out, "q_out", N, nq, d)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    for w in (k_weight, q_weight):
-        if w is not None and (w.dtype != torch.bfloat16 or w.shape != (d,) or not w.is_contiguous()):
-            raise TypeError("the norm weights must be contiguous bfloat16 [head_dim]")
-    dev = _on_device(k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, k_weight, q, q_weight, q_out, k_scale,
-                     v_scale, dev_err)
+    index = _on_device(k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, k_weight, q, q_weight, q_out, k_scale,
+                       v_scale, dev_err)
     if q is not None and q_out is None:
-        q_out = _empty(q.shape, torch.bfloat16, dev, stream)
+        q_out = _empty(q.shape, _BF16, index, stream)
         out_stride = nq * d
-    _run(lib().pkv_store_kvcache_norm_rope, "pkv_store_kvcache_norm_rope", dev, stream, _addr(q), q_stride,
-         _addr(q_out), out_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, _addr(q_weight), _addr(k_weight),
-         eps, _addr(k_cache), _addr(v_cache), _addr(slot_mapping), _addr(positions), _addr(cos_sin), cos_sin.shape[0],
-         style, N, nq, nkv, d, bs, nblk, dt, _addr(k_scale), _addr(v_scale), _addr(dev_err))
+    _run((_lib or lib()).pkv_store_kvcache_norm_rope, "pkv_store_kvcache_norm_rope", index, stream, _addr(q), q_stride,
+         _addr(q_out), out_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, _addr(q_weight),
+         k_weight.data_ptr(), eps, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+         positions.data_ptr(), cos_sin.data_ptr(), max_position, style, N, nq, nkv, d, bs, nblk, dt, _addr(k_scale),
+         _addr(v_scale), _addr(dev_err))
     return q_out
 
 
@@ -590,7 +600,7 @@ def paged_attention_tree(q, k_cache, v_cache, block_tables, cu_q_lens, context_l
     the number of thread blocks (0: chosen). A workspace is
     allocated when the plan (``plan_tree``) needs one and none is given; calls
     that may overlap need workspaces of their own."""
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+    if q.dtype != _BF16 or q.dim() != 3 or not q.is_contiguous():
         raise TypeError("q must be contiguous bfloat16 [total_q, heads, head_dim]")
     dt = _pool_args(k_cache, v_cache, k_scale, v_scale)
     T, nq, d = q.shape
@@ -606,21 +616,22 @@ def paged_attention_tree(q, k_cache, v_cache, block_tables, cu_q_lens, context_l
     _i32(tree_mask, "tree_mask", (T, words))
     if max_context_len is None:
         max_context_len = maxb * bs
-    if out is not None and (out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous()):
+    if out is not None and (out.shape != q.shape or out.dtype != _BF16 or not out.is_contiguous()):
         raise ValueError("out must be contiguous bfloat16 shaped like q")
-    dev = _on_device(q, k_cache, v_cache, block_tables, cu_q_lens, context_lens, tree_mask, out, k_scale, v_scale,
-                     workspace, dev_err)
+    index = _on_device(q, k_cache, v_cache, block_tables, cu_q_lens, context_lens, tree_mask, out, k_scale, v_scale,
+                       workspace, dev_err)
     if out is None:
-        out = _empty(q.shape, torch.bfloat16, dev, stream)
+        out = _empty(q.shape, _BF16, index, stream)
     if workspace is None:
         need = plan_tree(S, nq, nkv, d, bs, max_q_len, max_context_len, dt, shares)["workspace_bytes"]
         if need:
-            workspace = _empty(need, torch.uint8, dev, stream)
+            workspace = _empty(need, _U8, index, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _run(lib().pkv_paged_attention_tree, "pkv_paged_attention_tree", dev, stream, _addr(q), _addr(k_cache),
-         _addr(v_cache), _addr(block_tables), maxb, _addr(cu_q_lens), _addr(context_lens), _addr(tree_mask), words, S,
-         T, nq, nkv, d, bs, nblk, scale, dt, _addr(k_scale), _addr(v_scale), max_q_len, max_context_len,
-         shares, _addr(workspace), ws_bytes, _addr(out), _addr(dev_err))
+    _run((_lib or lib()).pkv_paged_attention_tree, "pkv_paged_attention_tree", index, stream, q.data_ptr(),
+         k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), maxb, cu_q_lens.data_ptr(),
+         context_lens.data_ptr(), tree_mask.data_ptr(), words, S, T, nq, nkv, d, bs, nblk, scale, dt, _addr(k_scale),
+         _addr(v_scale), max_q_len, max_context_len, shares, _addr(workspace), ws_bytes, out.data_ptr(),
+         _addr(dev_err))
     return out
 
 
@@ -642,11 +653,12 @@ def compact_kvcache(k_cache, v_cache, block_tables, cu_q_lens, context_lens, acc
     maxb, most = block_tables.shape[1], accepted.shape[1]
     _i32(block_tables, "block_tables", (S, maxb))
     _i32(accepted, "accepted", (S, most))
-    dev = _on_device(k_cache, v_cache, block_tables, cu_q_lens, context_lens, accepted, num_accepted, k_scale, v_scale,
-                     dev_err)
-    _run(lib().pkv_compact_kvcache, "pkv_compact_kvcache", dev, stream, _addr(k_cache), _addr(v_cache),
-         _addr(block_tables), maxb, _addr(cu_q_lens), _addr(context_lens), _addr(accepted), most, _addr(num_accepted),
-         S, nkv, d, bs, nblk, dt, _addr(k_scale), _addr(v_scale), _addr(dev_err))
+    index = _on_device(k_cache, v_cache, block_tables, cu_q_lens, context_lens, accepted, num_accepted, k_scale,
+                       v_scale, dev_err)
+    _run((_lib or lib()).pkv_compact_kvcache, "pkv_compact_kvcache", index, stream, k_cache.data_ptr(),
+         v_cache.data_ptr(), block_tables.data_ptr(), maxb, cu_q_lens.data_ptr(), context_lens.data_ptr(),
+         accepted.data_ptr(), most, num_accepted.data_ptr(), S, nkv, d, bs, nblk, dt, _addr(k_scale), _addr(v_scale),
+         _addr(dev_err))
 
 
 def load_kvcache(k_cache, v_cache, block_tables, cu_rows, total_rows=None, starts=None, k_out=None, v_out=None,
@@ -668,17 +680,17 @@ def load_kvcache(k_cache, v_cache, block_tables, cu_rows, total_rows=None, start
     if k_out is not None:
         T = k_out.shape[0]
         for t in (k_out, v_out):
-            if t.dtype != torch.bfloat16 or t.shape != (T, nkv, d) or not t.is_contiguous():
+            if t.dtype != _BF16 or t.shape != (T, nkv, d) or not t.is_contiguous():
                 raise ValueError("k_out and v_out must be contiguous bfloat16 [total_rows, num_kv_heads, head_dim]")
         if total_rows is not None and total_rows != T:
             raise ValueError("total_rows is not the outputs'")
-    dev = _on_device(k_cache, v_cache, block_tables, cu_rows, starts, k_out, v_out, k_scale, v_scale, dev_err)
+    index = _on_device(k_cache, v_cache, block_tables, cu_rows, starts, k_out, v_out, k_scale, v_scale, dev_err)
     if k_out is None:
         T = int(total_rows)
-        k_out, v_out = (_empty((T, nkv, d), torch.bfloat16, dev, stream) for _ in range(2))
-    _run(lib().pkv_load_kvcache, "pkv_load_kvcache", dev, stream, _addr(k_cache), _addr(v_cache), _addr(block_tables),
-         maxb, _addr(cu_rows), _addr(starts), S, T, nkv, d, bs, nblk, dt, _addr(k_scale), _addr(v_scale),
-         _addr(k_out), _addr(v_out), _addr(dev_err))
+        k_out, v_out = (_empty((T, nkv, d), _BF16, index, stream) for _ in range(2))
+    _run((_lib or lib()).pkv_load_kvcache, "pkv_load_kvcache", index, stream, k_cache.data_ptr(), v_cache.data_ptr(),
+         block_tables.data_ptr(), maxb, cu_rows.data_ptr(), _addr(starts), S, T, nkv, d, bs, nblk, dt, _addr(k_scale),
+         _addr(v_scale), k_out.data_ptr(), v_out.data_ptr(), _addr(dev_err))
     return k_out, v_out
 
 

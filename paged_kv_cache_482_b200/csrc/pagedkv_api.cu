@@ -499,7 +499,12 @@ int pkv_plan_tree(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
     if (st != PKV_OK) return st;
     if (shares < 0 || shares > kMaxTreeShares) return PKV_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads;
-    plan->shares = shares > 0 ? shares : pkv::tree_ctas_per_sm(max_q_len, group) * num_sms();
+    plan->shares = shares;
+    if (shares == 0) {  // one CTA per resident slot, fewer where the work cannot fill them
+        const long long most = pkv::tree_max_shares(num_seqs, num_kv_heads, group, max_q_len, max_context_len);
+        const long long resident = (long long)pkv::tree_ctas_per_sm(max_q_len, group) * num_sms();
+        plan->shares = (int)(most < resident ? most : resident);
+    }
     plan->workspace_bytes = 0;
     if (plan->shares > 1) {
         const size_t rows = (size_t)2 * plan->shares * pkv::tree_slot_rows(max_q_len, group);

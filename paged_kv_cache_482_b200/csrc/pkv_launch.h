@@ -261,6 +261,7 @@ int tree_unit_rows(int max_q_len, int group);
 int tree_slot_rows(int max_q_len, int group);
 int tree_ctas_per_sm(int max_q_len, int group);
 int tree_min_share();
+long long tree_max_shares(int num_seqs, int num_kv_heads, int group, int max_q_len, int max_context_len);
 
 bool prefill_supported(int head_dim, int group);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);

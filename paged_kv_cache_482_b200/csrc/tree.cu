@@ -82,7 +82,6 @@ struct Tree {
     static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
     static constexpr int kProducerWarp = kSoftmaxWarps;
     static constexpr int kMmaWarp = kSoftmaxWarps + 1;
-    static constexpr int kFirstConvWarp = kSoftmaxWarps + 2;
     static constexpr int kConvWarps = 2 * NT;
     static constexpr int kThreads = 32 * (kSoftmaxWarps + 2 + (kFp8 ? kConvWarps : 0));
     static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
@@ -126,6 +125,7 @@ struct TreeBars {
     int nonfinite[2];  // by unit parity: a draft's V held an infinity or NaN
     int bad[2];        // by unit parity: a block id outside the pool
     int failed;        // a softmax wait gave up
+    int unserved;      // some sequence cannot be served
     long long scan[16];  // share computation
 };
 static_assert(sizeof(TreeBars<2>) <= 512, "barrier space");
@@ -200,7 +200,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&w)[8])
 constexpr int kUnitCost = 4;
 // Shares are at least this long where the number of shares is chosen here: a
 // shorter one spends most of its time starting and joining.
-constexpr int kMinShare = 4;
+constexpr int kMinShare = 2;
 
 // A sequence's work. invalid: lengths that cannot be served.
 struct Seq {
@@ -236,24 +236,32 @@ struct Unit {
     int slot;    // workspace slot of a cut unit, -1 of a whole one
 };
 
-// All shares: share b is [b total / shares, (b + 1) total / shares) of the laid
-// out cost; the tiles of a unit at cost p lie at p + kUnitCost and behind.
+// All shares: the laid out cost is cut into equal ranges (the first total %
+// shares of them one longer); the tiles of a unit at cost p lie at p +
+// kUnitCost and behind.
 struct Shares {
-    long long total;
-    int shares;
-    __device__ __forceinline__ long long begin(int b) const { return total * b / shares; }
+    long long total, each;
+    int shares, longer;
+    __device__ __forceinline__ long long begin(int b) const { return each * b + min(b, longer); }
 };
+
+// x / y for x >= 0, y > 0: in 32 bits where that does (64-bit divisions are long code).
+__device__ __forceinline__ long long divide(long long x, int y) {
+    return (x >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+}
 
 // The total cost, and the sequence that holds the border `index` of the shares
 // (its begin) with the cost before it; for every thread of the block. `scratch`
-// is shared memory for 16 values.
+// is shared memory for 16 values; *unserved (shared memory) is set where a
+// sequence cannot be served.
 template <int THREADS>
 __device__ __forceinline__ Shares find_share(const TreeArgs &a, int log2_g, int index, long long *scratch, int &seq,
-                                             long long &before) {
+                                             long long &before, int *unserved = nullptr) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Shares sh;
-    sh.total = 0;
+    sh.total = sh.each = 0;
     sh.shares = 1;
+    sh.longer = 0;
     long long at = 0, cost = 0, done = 0, x = -1;
     const int chunks = (a.num_seqs + THREADS - 1) / THREADS;
     seq = 0;
@@ -264,7 +272,12 @@ __device__ __forceinline__ Shares find_share(const TreeArgs &a, int log2_g, int 
         const int s = (i < chunks ? i : i - chunks) * THREADS + threadIdx.x;
         if (chunks > 1 || i == 0) {
             if (i == chunks) done = 0;
-            cost = s < a.num_seqs ? load_seq(a, s, log2_g).cost(a.num_kv_heads) : 0;
+            cost = 0;
+            if (s < a.num_seqs) {
+                const Seq q = load_seq(a, s, log2_g);
+                cost = q.cost(a.num_kv_heads);
+                if (unserved && (q.lost || q.invalid)) *unserved = 1;
+            }
             long long inc = cost;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -283,8 +296,10 @@ __device__ __forceinline__ Shares find_share(const TreeArgs &a, int log2_g, int 
         }
         if (i == chunks - 1) {
             sh.total = done;
-            const long long most = done / a.min_share;
+            const long long most = divide(done, a.min_share);
             sh.shares = static_cast<int>(most < 1 ? 1 : most < a.max_shares ? most : a.max_shares);
+            sh.each = divide(done, sh.shares);
+            sh.longer = static_cast<int>(done - sh.each * sh.shares);
             if (done == 0 || index >= sh.shares) return sh;
             x = sh.begin(index);
         }
@@ -322,7 +337,7 @@ struct Walk {
         s = seq;
         q = load_seq(a, s, log2_g);
         rows = unit_rows;
-        k = static_cast<int>((x0 - before) / (q.tiles + kUnitCost));
+        k = static_cast<int>(divide(x0 - before, q.tiles + kUnitCost));
         p = before + static_cast<long long>(k) * (q.tiles + kUnitCost);
     }
     __device__ __forceinline__ bool next(const TreeArgs &a, int log2_g, Unit &u) {
@@ -832,26 +847,29 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
         mbar_init(&bars->drained, 1);
         bars->nonfinite[0] = bars->nonfinite[1] = 0;
         bars->bad[0] = bars->bad[1] = 0;
-        bars->failed = 0;
+        bars->failed = bars->unserved = 0;
         fence_barrier_init();
-    }
-    // sequences that cannot be served: reported, and zeros where their rows can be located
-    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
-        const Seq q = load_seq(a, s, log2_g);
-        if ((q.lost || q.invalid) && tid == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
-        if (q.invalid) {
-            const long long n = static_cast<long long>(q.c) * a.num_q_heads * (D / 8);
-            uint4 *dst = static_cast<uint4 *>(a.out) + static_cast<long long>(q.q0) * a.num_q_heads * (D / 8);
-            for (long long i = tid; i < n; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
-        }
     }
     const int share = blockIdx.x;
     int seq;
     long long before;
-    const Shares sh = find_share<kThreads>(a, log2_g, share, bars->scan, seq, before);
+    __syncthreads();  // barriers and flags are set
+    const Shares sh = find_share<kThreads>(a, log2_g, share, bars->scan, seq, before, &bars->unserved);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (bars->unserved) {
+        // sequences that cannot be served: reported, and zeros where their rows can be located
+        for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
+            const Seq q = load_seq(a, s, log2_g);
+            if ((q.lost || q.invalid) && tid == 0) set_error(a.dev_err, PKV_DEVERR_BOUNDS);
+            if (q.invalid) {
+                const long long n = static_cast<long long>(q.c) * a.num_q_heads * (D / 8);
+                uint4 *dst = static_cast<uint4 *>(a.out) + static_cast<long long>(q.q0) * a.num_q_heads * (D / 8);
+                for (long long i = tid; i < n; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
     const uint32_t tmem = bars->tmem;
     const bool work = sh.total > 0 && share < sh.shares;
     Walk walk;
@@ -1052,7 +1070,7 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
         // ================================================ V converters
         constexpr int kCT = L::kConvWarps * 32;
         constexpr int kCPR = D / 16;  // 16-code chunks per row
-        const int ct = tid - 32 * L::kFirstConvWarp;
+        const int ct = tid - 32 * (L::kMmaWarp + 1);
         bool ok = true;
         while (ok && walk.next(a, log2_g, u)) {
             for (int j = 0; j < u.tiles; ++j) {
@@ -1127,7 +1145,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     if (sh.total == 0 || border >= sh.shares) return;
     const long long x = sh.begin(border);
     const Seq q = load_seq(a, s, log2_g);
-    const int k = static_cast<int>((x - p) / (q.tiles + kUnitCost));
+    const int k = static_cast<int>(divide(x - p, q.tiles + kUnitCost));
     p += static_cast<long long>(k) * (q.tiles + kUnitCost);
     const int cut = tiles_before(x, p, q.tiles);
     if (cut == 0 || cut == q.tiles) return;
@@ -1244,6 +1262,14 @@ int tree_slot_rows(int max_q_len, int group) {
     return rows < unit ? static_cast<int>(rows) : unit;
 }
 int tree_min_share() { return kMinShare; }
+// The most shares that lengths within these bounds can make.
+long long tree_max_shares(int num_seqs, int num_kv_heads, int group, int max_q_len, int max_context_len) {
+    const double units = static_cast<double>(num_seqs) * num_kv_heads *
+                         ((static_cast<long long>(max_q_len) * group + tree_unit_rows(max_q_len, group) - 1) /
+                          tree_unit_rows(max_q_len, group));
+    const double shares = units * ((max_context_len + kBN - 1) / kBN + kUnitCost) / kMinShare;
+    return shares < 1 ? 1 : shares > 1e9 ? 1000000000LL : static_cast<long long>(shares);
+}
 
 namespace {
 

@@ -473,27 +473,25 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                 float x[W];
 #pragma unroll
                 for (int i = 0; i < W / 16; ++i) tmem_wait16(next[i]);
+                // scaled by the row's scale, or by the keys' own (then the row's enters below);
+                // the product frees the registers for the next load
 #pragma unroll
-                for (int i = 0; i < W; i += 2) {
-                    const float2 y = __fmul2_rn(make_float2(__uint_as_float(next[i / 16][i % 16]),
-                                                            __uint_as_float(next[i / 16][i % 16 + 1])),
-                                                make_float2(sl2, sl2));
+                for (int i = 0; i < W; i += 4) {
+                    float4 k4 = make_float4(sl2, sl2, sl2, sl2);
+                    if constexpr (MODE == 2) k4 = *reinterpret_cast<const float4 *>(ks + c + i);
+                    const uint32_t *n4 = &next[i / 16][i % 16];
+                    const float2 y = __fmul2_rn(make_float2(__uint_as_float(n4[0]), __uint_as_float(n4[1])),
+                                                make_float2(k4.x, k4.y));
+                    const float2 z = __fmul2_rn(make_float2(__uint_as_float(n4[2]), __uint_as_float(n4[3])),
+                                                make_float2(k4.z, k4.w));
                     x[i] = y.x;
                     x[i + 1] = y.y;
+                    x[i + 2] = z.x;
+                    x[i + 3] = z.y;
                 }
                 if (c + W < col0 + cols) {
 #pragma unroll
                     for (int i = 0; i < W / 16; ++i) tmem_ld16(ts + c + W + 16 * i, next[i]);
-                }
-                if constexpr (MODE == 2) {
-#pragma unroll
-                    for (int i = 0; i < W; i += 4) {
-                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + c + i);
-                        x[i] *= k4.x;
-                        x[i + 1] *= k4.y;
-                        x[i + 2] *= k4.z;
-                        x[i + 3] *= k4.w;
-                    }
                 }
                 if (special) {
                     const uint32_t vis = live ? visible32(mask, u.c, kv0 + c, u.base) : 0u;
@@ -506,7 +504,7 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                 for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(x[k], x[k + 4]), fmaxf(x[k + 8], x[k + 12]));
 #pragma unroll
                 for (int i = 16; i < W; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const float mx = (MODE == 2 ? sl2 : 1.0f) * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));  // sl2 > 0
                 const bool grow = mx > m + 8.0f;
                 if (__any_sync(0xffffffffu, grow)) {
                     // a new reference: what was formed with the old one is scaled
@@ -548,8 +546,9 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                     uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        float2 y = __fadd2_rn(make_float2(x[16 * h + 2 * i], x[16 * h + 2 * i + 1]),
-                                                    make_float2(ref, ref));
+                        float2 y = make_float2(x[16 * h + 2 * i], x[16 * h + 2 * i + 1]);
+                        y = MODE == 2 ? __ffma2_rn(y, make_float2(sl2, sl2), make_float2(ref, ref))
+                                      : __fadd2_rn(y, make_float2(ref, ref));
                         y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                         w[i] = pack_p<kF16>(y.x, y.y);
                         l2[i & 1] = __fadd2_rn(l2[i & 1], y);
@@ -626,31 +625,6 @@ __device__ __forceinline__ void add_nonfinite(const TreeArgs &a, const Unit &u, 
     for (int i = 0; i < N; ++i) v[i] = t[i];
 }
 
-// N result elements (a multiple of 4) from column col of a unit's row: bf16
-// output, or the binary32 partial of a cut unit.
-template <int D, int MODE, int N>
-__device__ __forceinline__ void emit(const TreeArgs &a, const Unit &u, bool nonfinite, int draft, __nv_bfloat16 *out,
-                                     float *part, int col, float (&v)[N]) {
-    if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, col, v);
-    if (u.slot < 0) {
-        uint32_t w[N / 2];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        if constexpr (N % 8 == 0) {
-#pragma unroll
-            for (int i = 0; i < N / 2; i += 4)
-                *reinterpret_cast<uint4 *>(out + col + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N / 2; i += 2) *reinterpret_cast<uint2 *>(out + col + 2 * i) = make_uint2(w[i], w[i + 1]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4)
-            *reinterpret_cast<float4 *>(part + col + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    }
-}
-
 // Results of a unit: normalised, the copies joined (through shared memory, 16
 // columns at a time), written as bf16 or as the partial, maximum and sum of a
 // cut unit.
@@ -684,39 +658,46 @@ __device__ __forceinline__ void write_unit(const TreeArgs &a, const Unit &u, Tre
     if (u.slot >= 0 && live && copy == 0)
         *reinterpret_cast<float2 *>(a.part_ml + prow * 2) = make_float2(top, bad ? -1.0f : sum);
     const uint32_t to = tmem + (warp >> 2) * 256 + 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float *mine = o + tid * L::kOutStride;
 #pragma unroll 1
     for (int col = 0; col < D; col += 16) {
         uint32_t w[16];
-        float v[16];
         tmem_ld16(to + col, w);
         tmem_wait16(w);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = drop ? 0.0f : __uint_as_float(w[i]) * f;
-        if (u.copies == 1) {
-            if (live) emit<D, MODE>(a, u, nonfinite, draft, out, part, col, v);
-            continue;
-        }
+        for (int i = 0; i < 16; ++i) w[i] = drop ? 0u : __float_as_uint(__uint_as_float(w[i]) * f);
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4 *>(o + tid * L::kOutStride + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        named_sync(1, kThreads);
+            *reinterpret_cast<uint4 *>(mine + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        if (u.copies > 1) named_sync(1, kThreads);  // else each thread reads its own row
         if (live) {
-            // 16 columns of the row, 4 at a time over the copies' threads
-            for (int c4 = copy; c4 < 4; c4 += u.copies) {
-                float4 y = *reinterpret_cast<const float4 *>(o + r * L::kOutStride + 4 * c4);
-                for (int k = 1; k < u.copies; ++k) {
-                    const float4 z =
-                        *reinterpret_cast<const float4 *>(o + (k * u.per_copy + r) * L::kOutStride + 4 * c4);
-                    y.x += z.x;
-                    y.y += z.y;
-                    y.z += z.z;
-                    y.w += z.w;
+#pragma unroll 1
+            for (int c8 = 8 * copy; c8 < 16; c8 += 8 * u.copies) {
+                float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+                for (int k = r; k < kUnitRows; k += u.per_copy) {
+                    const float4 y = *reinterpret_cast<const float4 *>(o + k * L::kOutStride + c8);
+                    const float4 z = *reinterpret_cast<const float4 *>(o + k * L::kOutStride + c8 + 4);
+                    x[0] += y.x;
+                    x[1] += y.y;
+                    x[2] += y.z;
+                    x[3] += y.w;
+                    x[4] += z.x;
+                    x[5] += z.y;
+                    x[6] += z.z;
+                    x[7] += z.w;
                 }
-                float x[4] = {y.x, y.y, y.z, y.w};
-                emit<D, MODE>(a, u, nonfinite, draft, out, part, col + 4 * c4, x);
+                if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, col + c8, x);
+                if (u.slot < 0) {
+                    *reinterpret_cast<uint4 *>(out + col + c8) = make_uint4(
+                        pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                } else {
+                    *reinterpret_cast<float4 *>(part + col + c8) = make_float4(x[0], x[1], x[2], x[3]);
+                    *reinterpret_cast<float4 *>(part + col + c8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                }
             }
         }
-        named_sync(1, kThreads);
+        if (u.copies > 1) named_sync(1, kThreads);
     }
     named_sync(1, kThreads);  // the flags are read
     if (tid == 0) {
@@ -767,9 +748,13 @@ __device__ __forceinline__ float load_queries(const TreeArgs &a, const Unit &u, 
         // of zero to binary32 against any finite key.
         const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 126;
         const int kq = min(60, 8 - e);
-        const float qs = __int_as_float((kq + 127) << 23);
+        float qs = __int_as_float((kq + 127) << 23);
         sl2 *= __int_as_float((127 - kq) << 23);
-        if (MODE == 1) sl2 *= __ldg(a.k_scale + u.kh);
+        if (MODE == 1) {  // the scale's sign goes into the queries, so that sl2 stays positive
+            const float ks = __ldg(a.k_scale + u.kh);
+            sl2 *= fabsf(ks);
+            if (ks < 0.0f) qs = -qs;
+        }
         if (!(amax <= 3.4e38f)) sl2 = __int_as_float(0x7FC00000);  // an infinite query: E4M3 has none
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {  // 16 elements: one chunk of hi and of lo
@@ -805,7 +790,7 @@ __device__ __forceinline__ float load_queries(const TreeArgs &a, const Unit &u, 
     if constexpr (!L::kFp8) cp_async_wait0();
     fence_proxy_async_smem();
     mbar_arrive(&bars->q_full);
-    return sl2;
+    return sl2 < 1.17549435e-38f ? 1.17549435e-38f : sl2;  // not 0, which a masked score's -inf turns into NaN
 }
 
 template <int D, int MODE, int NT>
@@ -1070,7 +1055,12 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
         // ================================================ V converters
         constexpr int kCT = L::kConvWarps * 32;
         constexpr int kCPR = D / 16;  // 16-code chunks per row
+        // a thread's chunks lie a multiple of 8 rows apart: one swizzle for all
+        constexpr int kRowStep = kCT / kCPR, kIters = kBN / kRowStep, kTogether = kIters < 4 ? kIters : 4;
+        static_assert(kRowStep % 8 == 0 && kIters % kTogether == 0, "whole steps");
         const int ct = tid - 32 * (L::kMmaWarp + 1);
+        const int row = ct / kCPR;
+        const uint32_t to_lo = swz(kBN, row, 2 * (ct % kCPR)), to_hi = swz(kBN, row, 2 * (ct % kCPR) + 1);
         bool ok = true;
         while (ok && walk.next(a, log2_g, u)) {
             for (int j = 0; j < u.tiles; ++j) {
@@ -1081,29 +1071,35 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
                     break;
                 }
                 const int end = min(kBN, u.t1 - (u.t0 + j * kBN));  // rows past the end become zeros
-                const uint8_t *src = sm + L::kR + rslot * L::kRSlot;
-                const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + rslot * kBN;
+                const uint32_t src = base + L::kR + rslot * L::kRSlot + ct * 16;
+                const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + rslot * kBN + row;
                 const uint32_t dst = base + L::kV + slot * L::kVSlot;
-#pragma unroll 2
-                for (int i0 = 0; i0 < kBN * kCPR; i0 += kCT) {
-                    const int i = i0 + ct;
-                    const int rr = i / kCPR, cc = i % kCPR;
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
-                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                    if (rr < end) {
+#pragma unroll
+                for (int i0 = 0; i0 < kIters; i0 += kTogether) {
+                    uint4 w[kTogether];
+#pragma unroll
+                    for (int i = 0; i < kTogether; ++i)
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                                     : "r"(src + (i0 + i) * kCT * 16));
+#pragma unroll
+                    for (int i = 0; i < kTogether; ++i) {
+                        const int down = (i0 + i) * kRowStep;  // rows below this thread's first
+                        uint4 lo, hi;
                         if constexpr (MODE == 2) {
-                            const float s = vs[rr];
-                            lo = e4m3x8_scaled_bf16x8(make_uint2(w.x, w.y), s);
-                            hi = e4m3x8_scaled_bf16x8(make_uint2(w.z, w.w), s);
+                            const float s = vs[down];
+                            lo = e4m3x8_scaled_bf16x8(make_uint2(w[i].x, w[i].y), s);
+                            hi = e4m3x8_scaled_bf16x8(make_uint2(w[i].z, w[i].w), s);
                         } else {
-                            const uint2 h0 = e4m3x4_to_f16x4(w.x), h1 = e4m3x4_to_f16x4(w.y);
-                            const uint2 h2 = e4m3x4_to_f16x4(w.z), h3 = e4m3x4_to_f16x4(w.w);
+                            const uint2 h0 = e4m3x4_to_f16x4(w[i].x), h1 = e4m3x4_to_f16x4(w[i].y);
+                            const uint2 h2 = e4m3x4_to_f16x4(w[i].z), h3 = e4m3x4_to_f16x4(w[i].w);
                             lo = make_uint4(h0.x, h0.y, h1.x, h1.y);
                             hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
                         }
+                        if (row + down >= end) lo = hi = make_uint4(0, 0, 0, 0);
+                        st_shared16(dst + to_lo + down * 128, lo);
+                        st_shared16(dst + to_hi + down * 128, hi);
                     }
-                    st_shared16(dst + swz(kBN, rr, 2 * cc), lo);
-                    st_shared16(dst + swz(kBN, rr, 2 * cc + 1), hi);
                 }
                 fence_proxy_async_smem();  // P V reads the tile through the async proxy
                 __syncwarp();

@@ -196,10 +196,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&w)[8])
                  : "memory");
 }
 
-// Cost of a unit besides its tiles (query loads, first scores, results), in tiles.
-constexpr int kUnitCost = 4;
+// Cost of a unit besides its tiles (query loads, first scores, results), in tiles
+// (64 ragged trees: 2: 91.7 us, 4: 87.4, 6: 86.0, 8: 86.7).
+constexpr int kUnitCost = 6;
 // Shares are at least this long where the number of shares is chosen here: a
-// shorter one spends most of its time starting and joining.
+// shorter one spends most of its time starting and joining (8 drafts on 500
+// tokens: 1: 14.2 us, 2: 13.2, 3: 13.7, 4: 15).
 constexpr int kMinShare = 2;
 
 // A sequence's work. invalid: lengths that cannot be served.
@@ -809,6 +811,8 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = a.block_size;
 
+    // the join kernel may take free slots now: it finds its borders meanwhile, and waits for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ------------------------------------------------ setup
     if (warp == L::kMmaWarp) tmem_alloc(smem_addr(&bars->tmem), L::kTmemCols);
     if (tid == 0) {
@@ -1116,7 +1120,6 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
 
     tc_fence_before();
     __syncthreads();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == L::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
@@ -1128,7 +1131,9 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
 // borders inside one unit divide its results among them). It may start before
 // the attention kernel has ended, and waits for that once it knows its part.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinSplit = 8;  // blocks per border: one block took 38 us for the results of 128 rows at a time
+// Blocks per border (64 ragged trees of 128 rows, both kernels: 1: 101 us, 2: 82, 4:
+// 79.6, 8: 83, 16: 94; most borders' blocks find nothing to join).
+constexpr int kJoinSplit = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int log2_g) {

@@ -46,9 +46,9 @@
 // significant bits, an E4M3 value 4, so the pair is exact down to 2^-9 of the
 // row's largest element and off by at most 2^-17 of it below), and S = hi K^T +
 // lo K^T in binary32 -- the tensor time of one 16-bit product, and no key is
-// converted. V is widened to f16 (exact) with a scale per KV head, where P is
-// rounded to f16, and to bf16(code * scale) with a scale per token, where P is
-// rounded to bf16 (V's range is then the scales'). The softmax runs in base 2
+// converted. V's codes are widened exactly, to f16 with a scale per KV head, where
+// P is rounded to f16, and to bf16 with a scale per token, where a weight times its
+// token's V scale is rounded to bf16 (whose range any scale fits). The softmax runs in base 2
 // with a reference maximum that moves only when a key exceeds it by 8; the normaliser
 // sums the weights in binary32 as they are before rounding.
 //
@@ -99,8 +99,8 @@ struct Tree {
     static constexpr uint32_t kV = kK + kNK * kKSlot;
     static constexpr uint32_t kR = kV + kNV * kVSlot;
     static constexpr uint32_t kKs = kR + kNR * kRSlot;  // per-token scales [slot][kBN] fp32
-    static constexpr uint32_t kVs = kKs + (MODE == 2 ? kNK * kBN * 4 : 0);
-    static constexpr uint32_t kBar = kVs + (MODE == 2 ? kNR * kBN * 4 : 0);
+    static constexpr uint32_t kVs = kKs + (MODE == 2 ? kNK * kBN * 4 : 0);  // both with the tile's K
+    static constexpr uint32_t kBar = kVs + (MODE == 2 ? kNK * kBN * 4 : 0);
     static constexpr uint32_t kMl = kBar + 512;  // [2][kUnitRows] fp32: maxima and sums of the copies
     static constexpr uint32_t kOut = kMl + 2 * kUnitRows * 4;  // [kUnitRows][kOutStride] fp32: 16 columns of the copies
     static constexpr int kOutStride = 20;
@@ -469,6 +469,7 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
             if (MODE == 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->k_full[g % L::kNK], (g / L::kNK) & 1)))
                 return false;
             const float *ks = reinterpret_cast<const float *>(sm + L::kKs) + (g % L::kNK) * kBN;
+            const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + (g % L::kNK) * kBN;
             float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
             for (int c = col0; c < col0 + cols; c += W) {
@@ -495,8 +496,9 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
 #pragma unroll
                     for (int i = 0; i < W / 16; ++i) tmem_ld16(ts + c + W + 16 * i, next[i]);
                 }
+                uint32_t vis = 0xffffffffu;
                 if (special) {
-                    const uint32_t vis = live ? visible32(mask, u.c, kv0 + c, u.base) : 0u;
+                    vis = live ? visible32(mask, u.c, kv0 + c, u.base) : 0u;
 #pragma unroll
                     for (int i = 0; i < W; ++i)
                         if (!((vis >> i) & 1u)) x[i] = -INFINITY;
@@ -552,8 +554,15 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                         y = MODE == 2 ? __ffma2_rn(y, make_float2(sl2, sl2), make_float2(ref, ref))
                                       : __fadd2_rn(y, make_float2(ref, ref));
                         y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        w[i] = pack_p<kF16>(y.x, y.y);
                         l2[i & 1] = __fadd2_rn(l2[i & 1], y);
+                        if constexpr (MODE == 2) {
+                            y = __fmul2_rn(y, *reinterpret_cast<const float2 *>(vs + c + 16 * h + 2 * i));
+                            if (special) {  // 0 times a scale that is not finite
+                                if (!((vis >> (16 * h + 2 * i)) & 1u)) y.x = 0.0f;
+                                if (!((vis >> (16 * h + 2 * i + 1)) & 1u)) y.y = 0.0f;
+                            }
+                        }
+                        w[i] = pack_p<kF16>(y.x, y.y);
                     }
                     tmem_st8(ts + c / 2 + 8 * h, w);
                 }
@@ -566,7 +575,7 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
         }
         if constexpr (MODE == 2) {
             // here, behind instructions that used every lane's scales: released right
-            // after the loads, the slot was refilled under lanes still reading it
+            // after their loads, the slot was refilled under lanes still reading it
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->k_empty[g % L::kNK]);
         }
@@ -609,8 +618,7 @@ __device__ __noinline__ void nonfinite_sum(const TreeArgs &a, const Unit &u, int
             if constexpr (MODE == 0) {
                 x = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.v_cache)[e]);
             } else {
-                x = e4m3x2_to_float2(static_cast<const uint8_t *>(a.v_cache)[e]).x;
-                if constexpr (MODE == 2) x = __bfloat162float(__float2bfloat16_rn(x * __ldg(a.v_scale + row)));
+                x = e4m3x2_to_float2(static_cast<const uint8_t *>(a.v_cache)[e]).x;  // a scale enters with the weights
             }
             if (!isfinite(x)) v[i] += x;
         }
@@ -931,7 +939,7 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
                     uint64_t *empty = is_k ? &bars->k_empty[slot] : kFp8 ? &bars->r_empty[slot] : &bars->v_empty[slot];
                     uint64_t *full = is_k ? &bars->k_full[slot] : kFp8 ? &bars->r_full[slot] : &bars->v_full[slot];
                     if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (use - 1) & 1))) return false;
-                    const uint32_t bytes = static_cast<uint32_t>(n * run) * (D * (kFp8 ? 1 : 2) + (MODE == 2 ? 4 : 0));
+                    const uint32_t bytes = static_cast<uint32_t>(n * run) * (D * (kFp8 ? 1 : 2) + (MODE == 2 && is_k ? 8 : 0));
                     if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                     __syncwarp();
                     if (mine) {
@@ -946,9 +954,10 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
                             else
                                 bulk_g2s(sm + L::kR + slot * L::kRSlot + bi * run * D,
                                          static_cast<const uint8_t *>(a.v_cache) + prow * D, run * D, full);
-                            if constexpr (MODE == 2)
-                                bulk_g2s(sm + (is_k ? L::kKs : L::kVs) + slot * kBN * 4 + bi * run * 4,
-                                         (is_k ? a.k_scale : a.v_scale) + prow, run * 4, full);
+                            if (MODE == 2 && is_k) {
+                                bulk_g2s(sm + L::kKs + slot * kBN * 4 + bi * run * 4, a.k_scale + prow, run * 4, full);
+                                bulk_g2s(sm + L::kVs + slot * kBN * 4 + bi * run * 4, a.v_scale + prow, run * 4, full);
+                            }
                         }
                     }
                     return true;
@@ -1076,7 +1085,6 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
                 }
                 const int end = min(kBN, u.t1 - (u.t0 + j * kBN));  // rows past the end become zeros
                 const uint32_t src = base + L::kR + rslot * L::kRSlot + ct * 16;
-                const float *vs = reinterpret_cast<const float *>(sm + L::kVs) + rslot * kBN + row;
                 const uint32_t dst = base + L::kV + slot * L::kVSlot;
 #pragma unroll
                 for (int i0 = 0; i0 < kIters; i0 += kTogether) {
@@ -1091,9 +1099,8 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
                         const int down = (i0 + i) * kRowStep;  // rows below this thread's first
                         uint4 lo, hi;
                         if constexpr (MODE == 2) {
-                            const float s = vs[down];
-                            lo = e4m3x8_scaled_bf16x8(make_uint2(w[i].x, w[i].y), s);
-                            hi = e4m3x8_scaled_bf16x8(make_uint2(w[i].z, w[i].w), s);
+                            lo = e4m3x8_to_bf16x8(make_uint2(w[i].x, w[i].y));
+                            hi = e4m3x8_to_bf16x8(make_uint2(w[i].z, w[i].w));
                         } else {
                             const uint2 h0 = e4m3x4_to_f16x4(w[i].x), h1 = e4m3x4_to_f16x4(w[i].y);
                             const uint2 h2 = e4m3x4_to_f16x4(w[i].z), h3 = e4m3x4_to_f16x4(w[i].w);

@@ -75,9 +75,9 @@ def tree_tolerance(out, mag, fp8, token):
     """Elementwise bound of the kernel's distance from tree_attention.
 
     The weights are rounded once before P V (bf16; f16 for E4M3 with a scale
-    per KV head) and the normaliser sums the rounded ones, so numerator and
-    normaliser are each off by u_p of their magnitude; per-token V is rounded
-    to bf16 when it is dequantised; the output to bf16. The binary32 sums and
+    per KV head), so the numerator is off by u_p of its magnitude, and the
+    normaliser, were it to sum the rounded ones, by u_p of its own; per-token V
+    may be rounded to bf16 when it is dequantised; the output is, too. The binary32 sums and
     the exponential add less than 2^-10 of the magnitude for the scores of
     these tests (below 2^6, with sums of at most 2^7 products).
     """

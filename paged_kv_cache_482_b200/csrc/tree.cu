@@ -549,20 +549,30 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                 for (int h = 0; h < W / 16; ++h) {
                     uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 y = make_float2(x[16 * h + 2 * i], x[16 * h + 2 * i + 1]);
-                        y = MODE == 2 ? __ffma2_rn(y, make_float2(sl2, sl2), make_float2(ref, ref))
-                                      : __fadd2_rn(y, make_float2(ref, ref));
-                        y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        l2[i & 1] = __fadd2_rn(l2[i & 1], y);
-                        if constexpr (MODE == 2) {
-                            y = __fmul2_rn(y, *reinterpret_cast<const float2 *>(vs + c + 16 * h + 2 * i));
-                            if (special) {  // 0 times a scale that is not finite
-                                if (!((vis >> (16 * h + 2 * i)) & 1u)) y.x = 0.0f;
-                                if (!((vis >> (16 * h + 2 * i + 1)) & 1u)) y.y = 0.0f;
-                            }
+                    for (int i = 0; i < 16; i += 4) {  // 4 keys
+                        float2 y[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            y[k] = make_float2(x[16 * h + i + 2 * k], x[16 * h + i + 2 * k + 1]);
+                            y[k] = MODE == 2 ? __ffma2_rn(y[k], make_float2(sl2, sl2), make_float2(ref, ref))
+                                             : __fadd2_rn(y[k], make_float2(ref, ref));
+                            y[k] = make_float2(fast_exp2(y[k].x), fast_exp2(y[k].y));
+                            l2[k] = __fadd2_rn(l2[k], y[k]);
                         }
-                        w[i] = pack_p<kF16>(y.x, y.y);
+                        if constexpr (MODE == 2) {
+                            float4 v4 = *reinterpret_cast<const float4 *>(vs + c + 16 * h + i);
+                            if (special) {  // not 0 times a scale that is not finite
+                                const uint32_t bits = vis >> (16 * h + i);
+                                if (!(bits & 1u)) v4.x = 0.0f;
+                                if (!(bits & 2u)) v4.y = 0.0f;
+                                if (!(bits & 4u)) v4.z = 0.0f;
+                                if (!(bits & 8u)) v4.w = 0.0f;
+                            }
+                            y[0] = __fmul2_rn(y[0], make_float2(v4.x, v4.y));
+                            y[1] = __fmul2_rn(y[1], make_float2(v4.z, v4.w));
+                        }
+                        w[i / 2] = pack_p<kF16>(y[0].x, y[0].y);
+                        w[i / 2 + 1] = pack_p<kF16>(y[1].x, y[1].y);
                     }
                     tmem_st8(ts + c / 2 + 8 * h, w);
                 }

@@ -483,7 +483,8 @@ PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int num_kv_heads, int h
  * Scores and sums are binary32; see the kernel for the operand types. Host
  * checks: as pkv_paged_attention_prefill (head_dim 64 or 128, group 1, 2, 4 or
  * 8, block_size a power of two in [8, 1024], scale positive and finite), plus
- * mask_words >= 1. Device checks: cu_q_lens that descends or leaves
+ * mask_words >= 1; pools of 2^31 or more (block, KV head, token) rows are
+ * PKV_ERR_UNSUPPORTED. Device checks: cu_q_lens that descends or leaves
  * [0, total_q] (the sequence's rows stay as they are), a chunk longer than
  * max_q_len or than its context, a context above max_context_len, or a block
  * id outside the pool (the sequence's rows are zeros) set PKV_DEVERR_BOUNDS.
@@ -520,7 +521,7 @@ PKV_API int pkv_paged_attention_tree(const void *q, const void *k_cache, const v
  *
  * No two sequences of a call may hold their drafts in the same slots. Host
  * checks: non-null pointers, 16-byte aligned caches, head_dim a multiple of 8,
- * sizes >= 1 (num_seqs may be 0). Device checks: anything out of range (a
+ * num_kv_heads * head_dim at most 2^26, sizes >= 1 (num_seqs may be 0). Device checks: anything out of range (a
  * length, a draft index, a list that does not ascend, a block id) sets
  * PKV_DEVERR_BOUNDS and leaves that sequence's rows as they are.
  */
@@ -543,7 +544,8 @@ PKV_API int pkv_compact_kvcache(void *k_cache, void *v_cache, const int32_t *blo
  *                no sequence (behind cu_rows[num_seqs]) are left as they are
  *
  * Host checks: non-null pointers, 16-byte aligned pools and outputs, head_dim
- * a multiple of 8, sizes >= 1 (num_seqs and total_rows may be 0). Device
+ * a multiple of 8, num_kv_heads * head_dim at most 2^26, sizes >= 1 (num_seqs
+ * and total_rows may be 0). Device
  * checks: cu_rows that descends or leaves [0, total_rows], a token outside
  * the table or a block id outside the pool (its rows are zeros) set
  * PKV_DEVERR_BOUNDS.

@@ -588,7 +588,7 @@ int pkv_compact_kvcache(void *k_cache, void *v_cache, const int32_t *block_table
         max_blocks_per_seq < 1 || max_accepted < 1)
         return PKV_ERR_INVALID_ARG;
     if (!valid_dtype(cache_dtype)) return PKV_ERR_INVALID_ARG;
-    if (num_blocks > INT32_MAX || head_dim > (1 << 20)) return PKV_ERR_INVALID_ARG;
+    if (num_blocks > INT32_MAX || (int64_t)num_kv_heads * head_dim > (1 << 26)) return PKV_ERR_INVALID_ARG;
     if (num_seqs == 0) return PKV_OK;
     if (!k_cache || !v_cache || !block_tables || !cu_q_lens || !context_lens || !accepted || !num_accepted)
         return PKV_ERR_INVALID_ARG;
@@ -626,7 +626,7 @@ int pkv_load_kvcache(const void *k_cache, const void *v_cache, const int32_t *bl
         num_blocks < 1 || max_blocks_per_seq < 1)
         return PKV_ERR_INVALID_ARG;
     if (!valid_dtype(cache_dtype)) return PKV_ERR_INVALID_ARG;
-    if (num_blocks > INT32_MAX || head_dim > (1 << 20)) return PKV_ERR_INVALID_ARG;
+    if (num_blocks > INT32_MAX || (int64_t)num_kv_heads * head_dim > (1 << 26)) return PKV_ERR_INVALID_ARG;
     if (num_seqs == 0 || total_rows == 0) return PKV_OK;
     if (!k_cache || !v_cache || !block_tables || !cu_rows || !k_out || !v_out) return PKV_ERR_INVALID_ARG;
     if (cache_dtype != PKV_CACHE_BF16 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;

@@ -292,6 +292,44 @@ def test_on_another_stream_with_its_own_workspace():
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
 
 
+@pytest.mark.parametrize("shares", [0, 50])
+def test_more_sequences_than_threads(shares):
+    """Lengths are summed in chunks of the block's threads."""
+    n = 700
+    ql = [(i * 5) % 4 for i in range(n)]  # some without drafts
+    c = make(ql, [q + (i * 11) % 150 + (q == 0) for i, q in enumerate(ql)], 4, 2, 64, 16, "bf16", seed=33)
+    check(c, shares=shares)
+
+
+def test_key_scales_of_either_sign_and_zero():
+    c = make([5, 40], [90, 300], 12, 3, 128, 16, "fp8", seed=34)
+    c["ks"][0] *= -1
+    c["ks"][1] = 0
+    check(c)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
+def test_queries_of_any_size(cache):
+    """Rows of zeros, of tiny and of large values; an infinite one is its own rows' matter."""
+    c = make([6, 9], [90, 200], 8, 2, 128, 16, cache, seed=35)
+    c["q"][0] = 0
+    c["q"][1] *= 2.0 ** -100
+    c["q"][2, :, ::7] *= 2.0 ** -30
+    c["q"][3] *= 2.0 ** 3
+    c["q"][7, 2, 5] = float("inf")
+    c["q"][8, 1, 3] = float("nan")
+    out = call(c)
+    ref, mag = reference(c)
+    hit = torch.zeros(15, 8, dtype=torch.bool)
+    hit[7, 2] = hit[8, 1] = True
+    g = out.double().cpu()
+    # scores up to 2^8 here: 2^-24 of that, summed over 2^7 products, moves a weight by less than 2^-10;
+    # E4M3 queries are off by 2^-17 of the row's largest, 2^-9 of a score unit in all
+    tol = R.tree_tolerance(ref, mag, cache != "bf16", cache == "fp8_token") + 2.0 ** -8 * mag
+    assert bool(((g - ref).abs() <= tol)[~hit].all())
+    assert bool(g[hit].isnan().all())
+
+
 def test_a_causal_chain_equals_prefill():
     """A tree that is a chain is a causal chunk: the prefill's result, to the roundings of both."""
     c = make([20, 50], [333, 1000], 8, 2, 128, 16, "bf16", seed=25)

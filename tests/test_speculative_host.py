@@ -86,6 +86,8 @@ def test_tree_abi_refusals(K):
     assert call(words=0) == K.PKV_ERR_INVALID_ARG
     assert call(mc=2049) == K.PKV_ERR_INVALID_ARG  # beyond the table
     assert call(mc=0) == K.PKV_ERR_INVALID_ARG
+    assert call(mq=65537, words=4096) == K.PKV_ERR_INVALID_ARG
+    assert call(mc=2**31 - 1, maxb=2**24) == K.PKV_ERR_INVALID_ARG
     assert call(part=-1) == K.PKV_ERR_INVALID_ARG and call(part=4097) == K.PKV_ERR_INVALID_ARG
     assert call(part=0) == K.PKV_ERR_WORKSPACE and call(part=2, ws=0x80000, wsb=64) == K.PKV_ERR_WORKSPACE
     assert call(part=2, ws=0x80010, wsb=1 << 30) == K.PKV_ERR_INVALID_ARG  # not 256-byte aligned
@@ -110,7 +112,7 @@ def test_compact_abi_refusals(K):
     for name in ("kc", "vc", "bt", "cu", "cl", "acc", "n"):
         assert call(**{name: None}) == K.PKV_ERR_INVALID_ARG, name
     for bad in (dict(kc=0x20008), dict(d=12), dict(d=0), dict(most=0), dict(maxb=0), dict(nblk=0), dict(bs=0),
-                dict(nkv=0), dict(S=-1), dict(dt=3), dict(dt=2), dict(nblk=2**31)):
+                dict(nkv=0), dict(S=-1), dict(dt=3), dict(dt=2), dict(nblk=2**31), dict(nkv=1 << 20)):
         assert call(**bad) == K.PKV_ERR_INVALID_ARG, bad
     assert call(S=0) == K.PKV_OK
     assert call(S=0, kc=None, acc=None) == K.PKV_OK
@@ -130,7 +132,7 @@ def test_load_abi_refusals(K):
     for name in ("kc", "vc", "bt", "cu", "ko", "vo"):
         assert call(**{name: None}) == K.PKV_ERR_INVALID_ARG, name
     for bad in (dict(kc=0x20008), dict(ko=0x70008), dict(d=12), dict(maxb=0), dict(nblk=0), dict(S=-1), dict(T=-1),
-                dict(dt=1), dict(dt=2), dict(dt=3), dict(nblk=2**31)):
+                dict(dt=1), dict(dt=2), dict(dt=3), dict(nblk=2**31), dict(nkv=1 << 20)):
         assert call(**bad) == K.PKV_ERR_INVALID_ARG, bad
     assert call(S=0) == K.PKV_OK and call(T=0) == K.PKV_OK
 

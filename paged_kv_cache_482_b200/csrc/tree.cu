@@ -712,8 +712,10 @@ __device__ __forceinline__ void write_unit(const TreeArgs &a, const Unit &u, Tre
                     *reinterpret_cast<uint4 *>(out + col + c8) = make_uint4(
                         pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
                 } else {
-                    *reinterpret_cast<float4 *>(part + col + c8) = make_float4(x[0], x[1], x[2], x[3]);
-                    *reinterpret_cast<float4 *>(part + col + c8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                    // whole 32-byte sectors (the workspace is 256-byte aligned)
+                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(part + col + c8),
+                                 "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                                 : "memory");
                 }
             }
         }

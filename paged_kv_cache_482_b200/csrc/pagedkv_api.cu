@@ -525,6 +525,7 @@ int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_c
                                  max_context_len, cache_dtype, shares, &plan);
     if (st != PKV_OK) return st;
     if (total_q < 0 || mask_words < 1 || (long long)mask_words * 32 < max_q_len) return PKV_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_q == 0) return PKV_OK;  // nothing to read: pointers may be NULL
     if (!q || !k_cache || !v_cache || !block_tables || !cu_q_lens || !context_lens || !tree_mask || !out)
         return PKV_ERR_INVALID_ARG;
     if (cache_dtype != PKV_CACHE_BF16 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
@@ -536,7 +537,6 @@ int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_c
         if (!workspace || workspace_bytes < plan.workspace_bytes) return PKV_ERR_WORKSPACE;
         if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_ERR_INVALID_ARG;
     }
-    if (num_seqs == 0 || total_q == 0) return PKV_OK;
     pkv::TreeArgs a;
     a.q = q;
     a.k_cache = k_cache;

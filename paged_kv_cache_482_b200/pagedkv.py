@@ -208,6 +208,11 @@ def _i32(t, name, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
+def _error_word(dev_err):
+    if dev_err is not None and (dev_err.dtype != _I32 or dev_err.numel() < 1):
+        raise TypeError("dev_err must be an int32 tensor of one element")
+
+
 def _on_device(*tensors) -> int:
     """The index of the one CUDA device that holds every given tensor."""
     index = tensors[0].get_device()  # -1 on the CPU
@@ -354,6 +359,7 @@ def store_kvcache_norm_rope(k, v, k_cache, v_cache, slot_mapping, positions, cos
             out_stride = _heads(q_out, "q_out", N, nq, d)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    _error_word(dev_err)
     index = _on_device(k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, k_weight, q, q_weight, q_out, k_scale,
                        v_scale, dev_err)
     if q is not None and q_out is None:
@@ -618,6 +624,9 @@ def paged_attention_tree(q, k_cache, v_cache, block_tables, cu_q_lens, context_l
         max_context_len = maxb * bs
     if out is not None and (out.shape != q.shape or out.dtype != _BF16 or not out.is_contiguous()):
         raise ValueError("out must be contiguous bfloat16 shaped like q")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _error_word(dev_err)
     index = _on_device(q, k_cache, v_cache, block_tables, cu_q_lens, context_lens, tree_mask, out, k_scale, v_scale,
                        workspace, dev_err)
     if out is None:
@@ -653,6 +662,7 @@ def compact_kvcache(k_cache, v_cache, block_tables, cu_q_lens, context_lens, acc
     maxb, most = block_tables.shape[1], accepted.shape[1]
     _i32(block_tables, "block_tables", (S, maxb))
     _i32(accepted, "accepted", (S, most))
+    _error_word(dev_err)
     index = _on_device(k_cache, v_cache, block_tables, cu_q_lens, context_lens, accepted, num_accepted, k_scale,
                        v_scale, dev_err)
     _run((_lib or lib()).pkv_compact_kvcache, "pkv_compact_kvcache", index, stream, k_cache.data_ptr(),
@@ -684,6 +694,7 @@ def load_kvcache(k_cache, v_cache, block_tables, cu_rows, total_rows=None, start
                 raise ValueError("k_out and v_out must be contiguous bfloat16 [total_rows, num_kv_heads, head_dim]")
         if total_rows is not None and total_rows != T:
             raise ValueError("total_rows is not the outputs'")
+    _error_word(dev_err)
     index = _on_device(k_cache, v_cache, block_tables, cu_rows, starts, k_out, v_out, k_scale, v_scale, dev_err)
     if k_out is None:
         T = int(total_rows)

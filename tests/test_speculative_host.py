@@ -95,6 +95,7 @@ def test_tree_abi_refusals(K):
     assert call(nblk=2**31) == K.PKV_ERR_INVALID_ARG
     assert call(S=-1) == K.PKV_ERR_INVALID_ARG and call(T=-1) == K.PKV_ERR_INVALID_ARG
     assert call(S=0) == K.PKV_OK and call(T=0) == K.PKV_OK
+    assert call(T=0, q=None, mask=None, out=None) == K.PKV_OK
 
 
 def test_compact_abi_refusals(K):
@@ -187,7 +188,8 @@ def test_python_refusals(K):
         tree()
     for bad in (dict(q=q.half()), dict(tree_mask=mask.long()), dict(tree_mask=mask[:2]), dict(cu_q_lens=cu[:2]),
                 dict(block_tables=tab[:1]), dict(q=q[:, :, :32].contiguous()), dict(out=q[:2]),
-                dict(q=q.transpose(0, 1)), dict(k_cache=kc.transpose(0, 1))):
+                dict(q=q.transpose(0, 1)), dict(k_cache=kc.transpose(0, 1)), dict(dev_err=torch.zeros(1)),
+                dict(workspace=torch.zeros(4, 4).t())):
         with pytest.raises((ValueError, TypeError)):
             tree(**bad)
 

@@ -1149,6 +1149,8 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
 // i and i + 1; if it cuts a unit, they make its part of that unit's results (the
 // borders inside one unit divide its results among them). It may start before
 // the attention kernel has ended, and waits for that once it knows its part.
+// Block 0 waits even with nothing to join: what the stream runs next is ordered
+// behind this kernel's end, which must not come before the attention kernel's.
 constexpr int kJoinThreads = 256;
 // Blocks per border (64 ragged trees of 128 rows, both kernels: 1: 101 us, 2: 82, 4:
 // 79.6, 8: 83, 16: 94; most borders' blocks find nothing to join).
@@ -1162,6 +1164,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     int s;
     long long p;
     const Shares sh = find_share<kJoinThreads>(a, log2_g, border, scratch, s, p);
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (sh.total == 0 || border >= sh.shares) return;
     const long long x = sh.begin(border);
     const Seq q = load_seq(a, s, log2_g);

@@ -362,3 +362,26 @@ def test_far_blocks_pass_32_bits():
     out = K.paged_attention_tree(small["q"], kp, vp, tab, small["cu"], small["ctx"], small["mask"], small["scale"],
                                  small["most"])
     assert torch.equal(out, want)
+
+
+def test_followed_by_a_copy_when_nothing_is_cut():
+    """Every share is exactly one unit, so there is nothing to join: a copy queued behind the call still
+    finds the finished rows, eagerly and replayed."""
+    S, nkv = 6, 2
+    c = make([16] * S, [16384] * S, 8, nkv, 128, 64, "bf16", 71)
+    ref, mag = reference(c)
+    plan = K.plan_tree(S, 8, nkv, 128, 64, c["most"], 16384, shares=S * nkv)
+    ws = torch.empty(plan["workspace_bytes"], dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(c["q"])
+    copy = torch.empty_like(out)
+
+    def step():
+        out.fill_(float("nan"))
+        call(c, out=out, workspace=ws, shares=S * nkv, max_context_len=16384)
+        copy.copy_(out)
+
+    for run in (step, K.graphed(step)):
+        for _ in range(5):
+            copy.zero_()
+            run()
+            close(c, copy, ref, mag)

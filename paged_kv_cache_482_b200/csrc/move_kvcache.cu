@@ -22,6 +22,9 @@ using tc::e4m3x8_scaled_bf16x8;
 // block, and writes them. accepted[i][j] >= j because the list ascends, so a
 // pass over places [a, b) writes only below b and every later pass reads only
 // at or above b: passes need nothing more between them.
+//
+// Latency bounds it: the chain lengths -> list -> table -> row -> store. Measured
+// (B200): one sequence of 8 drafts 2.7 us, 256 sequences of 33-64 drafts 7.2 us.
 constexpr int kMoveThreads = 256;
 
 // U: the copy unit (uint4, or uint2 where rows are not a multiple of 16 bytes).
@@ -103,6 +106,9 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(CompactArgs p) {
 // each row's sequence (by bisection over cu_rows) and pool block together, one
 // row per lane, and then move the rows' 16-byte output chunks, kLoadBatch of a
 // lane in flight.
+// Measured (B200): 16 sequences of 2048-8192 E4M3 tokens in blocks of 16, 8 heads of
+// 128: 88 us, 5.1 TB/s (a thread per chunk that finds its own sequence: 114 us); 133
+// bf16 tokens: 3.9 us.
 constexpr int kLoadThreads = 256;
 constexpr int kLoadRows = 8;  // at most; fewer while that leaves SMs without warps
 constexpr int kLoadBatch = 4;

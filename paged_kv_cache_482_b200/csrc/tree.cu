@@ -34,11 +34,14 @@
 // Between units the next queries are loaded (and their first scores formed)
 // before the results are written.
 //
-// Few rows: with at most a quarter (half) of the rows in use the unit holds 4 (2)
-// copies of them, and the warps of copy k handle the k-th quarter (half) of a tile's keys,
-// with weights of zero for the others: a copy is a split of the keys inside
-// the CTA, joined at the end of the unit. A thread then forms 16 (32)
-// exponentials per tile instead of 64.
+// Few rows: an E4M3 unit with at most half of its one row tile in use holds two copies
+// of its rows, and the warps of copy k handle the k-th half of a tile's keys, with weights
+// of zero for the other: a copy is a split of the keys inside the CTA, joined at the end
+// of the unit. 64 trees of 16 drafts on 1024-4096 tokens with per-token scales: 196 us,
+// without copies 245; 16 of 16 on 16384-32768 with a scale per head: 263 and 282. A bf16
+// unit never does (16 of 8 drafts on 16384-32768: with copies 290 us, without 276; 64 ragged
+// trees 79 and 74), nor one of two row tiles (head_dim 64: 41.8 and 40.1); four copies of a
+// quarter were slower than two.
 //
 // Operands: a bf16 cache feeds bf16 MMAs. E4M3 keys are the operand as they
 // are: Q, scaled per row by a power of two so that its largest element lies in
@@ -56,6 +59,15 @@
 // was, so its weight is zero; and V elements of drafts that are not finite are
 // set to zero in the staged tile (0 * inf would be NaN for the rows that do
 // not see the draft) and added to exactly the rows that see them at the end.
+//
+// Measured (B200, GPU time with the join, 32 query and 8 KV heads of 128):
+//   64 ragged trees of 1-32 drafts on 100-2048 bf16 tokens    79 us, 3.6 TB/s: in the
+//     loop the reads run near the copy rate; unit changes and uneven ends take the rest
+//   32 trees of 40-64 drafts on 1000-4096 bf16 tokens        134 us, 2.5 TB/s: two row
+//     tiles' exponentials and operand reads from shared memory, per key tile
+//   16 trees of 16 drafts on 16384-32768 E4M3 tokens         275 us, 2.9 TB/s: shared
+//     memory (hi and lo Q are read again for every 64 keys) and one copy per 16-token block
+//   one tree of 8 drafts on 500 bf16 tokens                   13 us: starts of two kernels
 //
 // Every wait is bounded (PKV_DEVERR_TIMEOUT); every block id and length is
 // checked before anything is copied (PKV_DEVERR_BOUNDS).
@@ -77,6 +89,7 @@ template <int D, int MODE, int NT>
 struct Tree {
     static constexpr bool kFp8 = MODE != 0;
     static constexpr bool kF16 = MODE == 1;  // type of P and V
+    static constexpr bool kTwoCopies = kFp8 && NT == 1;  // units of few rows may hold two copies
     static constexpr int kUnitRows = NT * kRows;
     static constexpr int kSoftmaxWarps = 4 * NT;
     static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
@@ -102,9 +115,9 @@ struct Tree {
     static constexpr uint32_t kVs = kKs + (MODE == 2 ? kNK * kBN * 4 : 0);  // both with the tile's K
     static constexpr uint32_t kBar = kVs + (MODE == 2 ? kNK * kBN * 4 : 0);
     static constexpr uint32_t kMl = kBar + 512;  // [2][kUnitRows] fp32: maxima and sums of the copies
-    static constexpr uint32_t kOut = kMl + 2 * kUnitRows * 4;  // [kUnitRows][kOutStride] fp32: 16 columns of the copies
-    static constexpr int kOutStride = 20;
-    static constexpr uint32_t kBytes = kOut + kUnitRows * kOutStride * 4;
+    static constexpr uint32_t kOut = kMl + 2 * kUnitRows * 4;  // two copies: [kRows][kOutStride] fp32, 8 columns
+    static constexpr int kOutStride = 12;
+    static constexpr uint32_t kBytes = kOut + (kTwoCopies ? kRows * kOutStride * 4 : 0);
     static constexpr uint32_t kMin = (NT == 1 ? 80u : 120u) * 1024u;  // no more CTAs per SM than tensor memory has room for
     static constexpr uint32_t kAlloc = kBytes + 1024 > kMin ? kBytes + 1024 : kMin;  // + base alignment
     static_assert(kCtasPerSm * (kAlloc + 1024) <= 228u * 1024u, "shared memory");
@@ -362,7 +375,7 @@ struct Walk {
             u.base = q.ctx - q.c;
             u.row0 = (kk % q.row_tiles) * rows;
             u.rows = min(rows, (q.c << log2_g) - u.row0);
-            u.copies = u.rows * 4 <= rows ? 4 : u.rows * 2 <= rows ? 2 : 1;
+            u.copies = a.mode != 0 && rows == kRows && u.rows * 2 <= rows ? 2 : 1;
             u.per_copy = rows / u.copies;
             u.t0 = tb * kBN;
             u.t1 = min(q.ctx, te * kBN);
@@ -436,8 +449,8 @@ template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float p0, float p1) { return F16 ? pack_f16(p0, p1) : pack_bf16(p0, p1); }
 
 // Softmax of this warp's rows over the unit's tiles: 64 / copies keys of every
-// tile, W at a time in a loop (written out for 64 keys, in one variant per
-// number of copies, the code outgrew the instruction cache: a CTA's first tile
+// tile, W at a time in a loop (written out for 64 keys the
+// code outgrew the instruction cache: a CTA's first tile
 // took 8000 cycles). g0: tiles of the units before. Leaves the reference maximum
 // and the sum of the row (copy).
 template <int D, int MODE, int NT, int W>
@@ -449,7 +462,7 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int half = warp >> 2;  // row tile
     const bool idle = !__any_sync(0xffffffffu, live);  // no row in this warp: its weights are never read
-    const int cols = kBN / u.copies, col0 = (warp * 32) / u.per_copy * cols;
+    const int cols = L::kTwoCopies ? kBN / u.copies : kBN, col0 = L::kTwoCopies ? (warp * 32) / u.per_copy * cols : 0;
     const uint32_t *mask = a.mask + static_cast<long long>(u.q0 + draft) * a.mask_words;
     const uint32_t tw = tmem + half * 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
     const uint32_t to = tw + 128;
@@ -678,26 +691,34 @@ __device__ __forceinline__ void write_unit(const TreeArgs &a, const Unit &u, Tre
     if (u.slot >= 0 && live && copy == 0)
         *reinterpret_cast<float2 *>(a.part_ml + prow * 2) = make_float2(top, bad ? -1.0f : sum);
     const uint32_t to = tmem + (warp >> 2) * 256 + 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float *mine = o + tid * L::kOutStride;
+    const bool two = L::kTwoCopies && u.copies == 2;
 #pragma unroll 1
     for (int col = 0; col < D; col += 16) {
         uint32_t w[16];
         tmem_ld16(to + col, w);
         tmem_wait16(w);
+        float v[2][8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = drop ? 0u : __float_as_uint(__uint_as_float(w[i]) * f);
+        for (int i = 0; i < 16; ++i) v[i / 8][i % 8] = drop ? 0.0f : __uint_as_float(w[i]) * f;
+        if (two) {  // copy k keeps the columns 8 k .. 8 k + 7 and hands over the others
+            float *mine = o + tid * L::kOutStride;
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<uint4 *>(mine + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-        if (u.copies > 1) named_sync(1, kThreads);  // else each thread reads its own row
+            for (int i = 0; i < 8; i += 4)
+                *reinterpret_cast<float4 *>(mine + i) =
+                    copy ? make_float4(v[0][i], v[0][i + 1], v[0][i + 2], v[0][i + 3])
+                         : make_float4(v[1][i], v[1][i + 1], v[1][i + 2], v[1][i + 3]);
+            named_sync(1, kThreads);
+        }
         if (live) {
 #pragma unroll 1
-            for (int c8 = 8 * copy; c8 < 16; c8 += 8 * u.copies) {
-                float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 1
-                for (int k = r; k < kUnitRows; k += u.per_copy) {
-                    const float4 y = *reinterpret_cast<const float4 *>(o + k * L::kOutStride + c8);
-                    const float4 z = *reinterpret_cast<const float4 *>(o + k * L::kOutStride + c8 + 4);
+            for (int h = copy; h < 2; h += u.copies) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = h ? v[1][i] : v[0][i];
+                if (two) {
+                    const float *other = o + (tid ^ (kRows / 2)) * L::kOutStride;
+                    const float4 y = *reinterpret_cast<const float4 *>(other);
+                    const float4 z = *reinterpret_cast<const float4 *>(other + 4);
                     x[0] += y.x;
                     x[1] += y.y;
                     x[2] += y.z;
@@ -707,19 +728,20 @@ __device__ __forceinline__ void write_unit(const TreeArgs &a, const Unit &u, Tre
                     x[6] += z.z;
                     x[7] += z.w;
                 }
-                if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, col + c8, x);
+                const int c8 = col + 8 * h;
+                if (nonfinite) add_nonfinite<D, MODE>(a, u, draft, c8, x);
                 if (u.slot < 0) {
-                    *reinterpret_cast<uint4 *>(out + col + c8) = make_uint4(
-                        pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                    *reinterpret_cast<uint4 *>(out + c8) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                                      pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
                 } else {
                     // whole 32-byte sectors (the workspace is 256-byte aligned)
-                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(part + col + c8),
-                                 "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(part + c8), "f"(x[0]),
+                                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                                  : "memory");
                 }
             }
         }
-        if (u.copies > 1) named_sync(1, kThreads);
+        if (two) named_sync(1, kThreads);
     }
     named_sync(1, kThreads);  // the flags are read
     if (tid == 0) {
@@ -898,10 +920,7 @@ __global__ void __launch_bounds__(Tree<D, MODE, NT>::kThreads, Tree<D, MODE, NT>
             const bool live = r < u.rows;
             const int draft = (u.row0 + (live ? r : 0)) >> log2_g;
             float m = -INFINITY, l = 0.0f;
-            const bool ok = u.copies == 4 ? softmax_tiles<D, MODE, NT, 16>(a, u, bars, sm, base, tmem, sl2, live, draft,
-                                                                           g, unit, m, l)
-                                          : softmax_tiles<D, MODE, NT, 32>(a, u, bars, sm, base, tmem, sl2, live, draft,
-                                                                           g, unit, m, l);
+            const bool ok = softmax_tiles<D, MODE, NT, 32>(a, u, bars, sm, base, tmem, sl2, live, draft, g, unit, m, l);
             if (!ok && lane == 0) {
                 set_error(a.dev_err, PKV_DEVERR_TIMEOUT);
                 bars->failed = 1;
@@ -1274,7 +1293,9 @@ cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
 }  // namespace
 
 // One or two row tiles per unit: two once a tree may have more rows than a tile
-// (they share every key tile then, and the call is bound by more than its reads).
+// (they share every key tile then). Trees of up to 256 rows: one 152 us, two 134; of
+// up to 168 rows, head_dim 64: 45.6 and 42.6. Of up to 128 rows: one 79.5 us, two 110;
+// of 64 rows on long contexts 272 and 460.
 int tree_unit_rows(int max_q_len, int group) {
     return static_cast<long long>(max_q_len) * group > kRows ? 2 * kRows : kRows;
 }

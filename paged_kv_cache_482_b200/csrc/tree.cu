@@ -61,11 +61,11 @@
 // not see the draft) and added to exactly the rows that see them at the end.
 //
 // Measured (B200, GPU time with the join, 32 query and 8 KV heads of 128):
-//   64 ragged trees of 1-32 drafts on 100-2048 bf16 tokens    79 us, 3.6 TB/s: in the
+//   64 ragged trees of 1-32 drafts on 100-2048 bf16 tokens    74 us, 3.9 TB/s: in the
 //     loop the reads run near the copy rate; unit changes and uneven ends take the rest
-//   32 trees of 40-64 drafts on 1000-4096 bf16 tokens        134 us, 2.5 TB/s: two row
+//   32 trees of 40-64 drafts on 1000-4096 bf16 tokens        128 us, 2.6 TB/s: two row
 //     tiles' exponentials and operand reads from shared memory, per key tile
-//   16 trees of 16 drafts on 16384-32768 E4M3 tokens         275 us, 2.9 TB/s: shared
+//   16 trees of 16 drafts on 16384-32768 E4M3 tokens         270 us, 3.0 TB/s: shared
 //     memory (hi and lo Q are read again for every 64 keys) and one copy per 16-token block
 //   one tree of 8 drafts on 500 bf16 tokens                   13 us: starts of two kernels
 //
@@ -449,10 +449,9 @@ template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float p0, float p1) { return F16 ? pack_f16(p0, p1) : pack_bf16(p0, p1); }
 
 // Softmax of this warp's rows over the unit's tiles: 64 / copies keys of every
-// tile, W at a time in a loop (written out for 64 keys the
-// code outgrew the instruction cache: a CTA's first tile
-// took 8000 cycles). g0: tiles of the units before. Leaves the reference maximum
-// and the sum of the row (copy).
+// tile, W at a time in a loop (written out for 64 keys the code outgrew the
+// instruction cache: a CTA's first tile took 8000 cycles). g0: tiles of the units
+// before. Leaves the reference maximum and the sum of the row (copy).
 template <int D, int MODE, int NT, int W>
 __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, TreeBars<NT> *bars, uint8_t *sm,
                                               uint32_t base, uint32_t tmem, float sl2, bool live, int draft,
@@ -1293,9 +1292,9 @@ cudaError_t launch_mode(const TreeArgs &a, cudaStream_t stream) {
 }  // namespace
 
 // One or two row tiles per unit: two once a tree may have more rows than a tile
-// (they share every key tile then). Trees of up to 256 rows: one 152 us, two 134; of
-// up to 168 rows, head_dim 64: 45.6 and 42.6. Of up to 128 rows: one 79.5 us, two 110;
-// of 64 rows on long contexts 272 and 460.
+// (they share every key tile then). Trees of up to 256 rows: one 144 us, two 127; of
+// up to 168 rows, head_dim 64: 41.2 either way. Of up to 128 rows: one 74.7 us, two 99.6;
+// of 64 rows on long contexts 270 and 421.
 int tree_unit_rows(int max_q_len, int group) {
     return static_cast<long long>(max_q_len) * group > kRows ? 2 * kRows : kRows;
 }

@@ -178,9 +178,9 @@ PKV_API int pkv_store_kvcache_rope(const void *q, void *q_out, const void *k, co
  * either may stay, and parts of both.
  *
  * Host checks: as pkv_store_kvcache_rope, plus strides that are multiples of
- * 8 elements and at least heads * head_dim, and eps >= 0 and finite. Device
- * checks: as there (a token at a position outside the table is not written at
- * all; slot -1 skips the cache write only).
+ * 8 elements and at least heads * head_dim, heads * head_dim at most 2^26, and
+ * eps >= 0 and finite. Device checks: as there (a token at a position outside
+ * the table is not written at all; slot -1 skips the cache write only).
  */
 PKV_API int pkv_store_kvcache_norm_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
                                         const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -483,11 +483,12 @@ PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int num_kv_heads, int h
  * Scores and sums are binary32; see the kernel for the operand types. Host
  * checks: as pkv_paged_attention_prefill (head_dim 64 or 128, group 1, 2, 4 or
  * 8, block_size a power of two in [8, 1024], scale positive and finite), plus
- * mask_words >= 1; pools of 2^31 or more (block, KV head, token) rows are
- * PKV_ERR_UNSUPPORTED. Device checks: cu_q_lens that descends or leaves
- * [0, total_q] (the sequence's rows stay as they are), a chunk longer than
- * max_q_len or than its context, a context above max_context_len, or a block
- * id outside the pool (the sequence's rows are zeros) set PKV_DEVERR_BOUNDS.
+ * mask_words >= 1 and 16-byte aligned per-token scale pools; pools of 2^31 or
+ * more (block, KV head, token) rows are PKV_ERR_UNSUPPORTED. Device checks:
+ * cu_q_lens that descends or leaves [0, total_q] (the sequence's rows stay as
+ * they are), a chunk longer than max_q_len or than its context, a context above
+ * max_context_len, or a block id outside the pool (the sequence's rows are
+ * zeros) set PKV_DEVERR_BOUNDS.
  */
 typedef struct {
     int shares;             /* thread blocks */
@@ -521,9 +522,10 @@ PKV_API int pkv_paged_attention_tree(const void *q, const void *k_cache, const v
  *
  * No two sequences of a call may hold their drafts in the same slots. Host
  * checks: non-null pointers, 16-byte aligned caches, head_dim a multiple of 8,
- * num_kv_heads * head_dim at most 2^26, sizes >= 1 (num_seqs may be 0). Device checks: anything out of range (a
- * length, a draft index, a list that does not ascend, a block id) sets
- * PKV_DEVERR_BOUNDS and leaves that sequence's rows as they are.
+ * num_kv_heads * head_dim at most 2^26, sizes >= 1 (num_seqs may be 0). Device
+ * checks: anything out of range (a length, a draft index, a list that does not
+ * ascend, a block id) sets PKV_DEVERR_BOUNDS and leaves that sequence's rows as
+ * they are.
  */
 PKV_API int pkv_compact_kvcache(void *k_cache, void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
                                 const int32_t *cu_q_lens, const int32_t *context_lens, const int32_t *accepted,
@@ -545,10 +547,9 @@ PKV_API int pkv_compact_kvcache(void *k_cache, void *v_cache, const int32_t *blo
  *
  * Host checks: non-null pointers, 16-byte aligned pools and outputs, head_dim
  * a multiple of 8, num_kv_heads * head_dim at most 2^26, sizes >= 1 (num_seqs
- * and total_rows may be 0). Device
- * checks: cu_rows that descends or leaves [0, total_rows], a token outside
- * the table or a block id outside the pool (its rows are zeros) set
- * PKV_DEVERR_BOUNDS.
+ * and total_rows may be 0). Device checks: cu_rows that descends or leaves
+ * [0, total_rows], a token outside the table or a block id outside the pool
+ * (its rows are zeros) set PKV_DEVERR_BOUNDS.
  */
 PKV_API int pkv_load_kvcache(const void *k_cache, const void *v_cache, const int32_t *block_tables,
                              int max_blocks_per_seq, const int32_t *cu_rows, const int32_t *starts, int num_seqs,

@@ -182,7 +182,8 @@ int pkv_store_kvcache_norm_rope(const void *q, int64_t q_stride, void *q_out, in
     if (!pow2(head_dim / 16) || head_dim > 512) return PKV_ERR_UNSUPPORTED;
     if (!(eps >= 0.0f) || eps > 3.0e38f) return PKV_ERR_INVALID_ARG;  // negative, NaN or infinite
     if ((q == nullptr) != (q_out == nullptr)) return PKV_ERR_INVALID_ARG;
-    if (q && num_q_heads < 1) return PKV_ERR_INVALID_ARG;
+    if (q && (num_q_heads < 1 || (int64_t)num_q_heads * head_dim > (1 << 26))) return PKV_ERR_INVALID_ARG;
+    if ((int64_t)num_kv_heads * head_dim > (1 << 26)) return PKV_ERR_INVALID_ARG;
     auto bad_stride = [&](int64_t stride, int heads) {
         return stride % 8 != 0 || stride < (int64_t)heads * head_dim || stride > (INT64_MAX >> 34);
     };
@@ -530,6 +531,9 @@ int pkv_paged_attention_tree(const void *q, const void *k_cache, const void *v_c
         return PKV_ERR_INVALID_ARG;
     if (cache_dtype != PKV_CACHE_BF16 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
+    // bulk copies read the scale pools
+    if (cache_dtype == PKV_CACHE_FP8_E4M3_TOKEN && (!aligned16(k_scale) || !aligned16(v_scale)))
+        return PKV_ERR_INVALID_ARG;
     if (max_blocks_per_seq < 1 || num_blocks < 1 || num_blocks > INT32_MAX) return PKV_ERR_INVALID_ARG;
     if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size) return PKV_ERR_INVALID_ARG;
     if (!(scale > 0.0f) || scale > 3.0e38f) return PKV_ERR_INVALID_ARG;  // positive and finite

@@ -46,6 +46,8 @@ def test_norm_rope_abi_refusals(K):
     assert call(vs_=512) == K.PKV_ERR_INVALID_ARG
     assert call(qs=4095) == K.PKV_ERR_INVALID_ARG and call(qos=2048) == K.PKV_ERR_INVALID_ARG
     assert call(qs=-4096) == K.PKV_ERR_INVALID_ARG
+    assert call(nq=2**20, qs=2**27, qos=2**27) == K.PKV_ERR_INVALID_ARG  # more than 2^26 elements a token
+    assert call(nkv=2**20, ks_=2**27, vs_=2**27) == K.PKV_ERR_INVALID_ARG
     for eps in (-1e-6, float("nan"), float("inf")):
         assert call(eps=eps) == K.PKV_ERR_INVALID_ARG
     assert call(mp=0) == K.PKV_ERR_INVALID_ARG
@@ -93,6 +95,9 @@ def test_tree_abi_refusals(K):
     assert call(part=2, ws=0x80010, wsb=1 << 30) == K.PKV_ERR_INVALID_ARG  # not 256-byte aligned
     assert call(S=0, part=2, ws=0x80000, wsb=1 << 30) == K.PKV_OK
     assert call(nblk=2**31) == K.PKV_ERR_INVALID_ARG
+    # scale pools are copied in 16-byte pieces; scales per head are read one by one
+    for bad in (dict(ks=0x80004), dict(vs=0x90008)):
+        assert call(dt=2, **{**dict(ks=0x80000, vs=0x90000), **bad}) == K.PKV_ERR_INVALID_ARG
     assert call(S=-1) == K.PKV_ERR_INVALID_ARG and call(T=-1) == K.PKV_ERR_INVALID_ARG
     assert call(S=0) == K.PKV_OK and call(T=0) == K.PKV_OK
     assert call(T=0, q=None, mask=None, out=None) == K.PKV_OK

@@ -202,7 +202,8 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
         : "memory");
 }
 
-// 8 columns into this thread's lane, not waited for.
+// 8 columns into this thread's lane, not waited for: tmem_wait_st() before the
+// columns are loaded again.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&w)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                  "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -523,7 +524,10 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                 const float mx = (MODE == 2 ? sl2 : 1.0f) * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));  // sl2 > 0
                 const bool grow = mx > m + 8.0f;
                 if (__any_sync(0xffffffffu, grow)) {
-                    // a new reference: what was formed with the old one is scaled
+                    // a new reference: what was formed with the old one is scaled. This tile's
+                    // earlier steps stored weights (and, if the reference grew, O) without waiting,
+                    // and nothing but this wait orders those stores before the loads below.
+                    tmem_wait_st();
                     const float alpha = grow ? fast_exp2(m - mx) : 1.0f;  // 0 from m = -inf
                     if (grow) {
                         m = mx;

@@ -385,3 +385,42 @@ def test_followed_by_a_copy_when_nothing_is_cut():
             copy.zero_()
             run()
             close(c, copy, ref, mag)
+
+
+def put(c, seq, first, k, v):
+    """Store rows k, v [n, nkv, d] as the tokens first .. first + n - 1 of a sequence."""
+    bs = c["kp"].shape[2]
+    t = torch.arange(first, first + k.shape[0])
+    slots = (c["tab"][seq].cpu().long()[t // bs] * bs + t % bs).int().cuda()
+    K.store_kvcache(k.bfloat16().cuda(), v.bfloat16().cuda(), c["kp"], c["vp"], slots, c["ks"], c["vs"])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("drafts", [8, 24, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_maxima_that_grow_in_every_half_of_a_tile(d, drafts, cache):
+    """Half of the heads meet scores that rise by more than 2^8 every 32 keys, the others scores that fall as
+    fast, so what a tile has stored of its weights and results is scaled twice within each tile. V grows
+    backwards by 2^8, so that the scaled parts weigh as much as the rest. Units of two copies (E4M3), of one
+    row tile, and of two."""
+    steps = 29
+    base = 32 * steps
+    c = make([drafts], [base + drafts], 8, 2, d, 16, cache, seed=41, words=2)
+    g = torch.Generator().manual_seed(42)
+    if cache == "fp8":
+        c["ks"].fill_(1.0)
+        c["vs"].fill_(1.0)
+    n = base + drafts
+    step = (torch.arange(n) // 32).clamp(max=steps - 1)
+    k = torch.randn(n, 2, d, generator=g)
+    k[:, :, 0] = (32.0 * (step - 14))[:, None]  # every one of them an E4M3 value
+    back = steps - 1 - step
+    size = torch.where(back == 0, 2.0 ** -8, torch.where(back == 1, 1.0, 256.0))
+    v = torch.where(torch.rand(n, 2, d, generator=g) < 0.5, -1.0, 1.0) * size[:, None, None]
+    put(c, 0, 0, k, v)
+    # a step is 32 * 2.25 / sqrt(d) * log2(e) = 9.2 (d 128) or 13 (d 64) powers of two, the others' share below 1
+    q = 0.25 * torch.randn(drafts, 8, d, generator=g)
+    q[:, :, 0] = torch.where(torch.arange(8) % 2 == 0, 2.25, -2.25)
+    c["q"].copy_(q.bfloat16())
+    for shares in (0, 1):
+        check(c, shares=shares)

@@ -480,8 +480,10 @@ PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int num_kv_heads, int h
  *  out            [total_q][num_q_heads][head_dim] bf16; rows at and beyond
  *                 cu_q_lens[num_seqs] are left as they are
  *
- * Scores and sums are binary32; see the kernel for the operand types. Host
- * checks: as pkv_paged_attention_prefill (head_dim 64 or 128, group 1, 2, 4 or
+ * Scores and sums are binary32; see the kernel for the operand types. In an
+ * E4M3 cache with a scale per KV head the weights are f16 operands: one below
+ * 2^-21 of its row's largest is off by up to 2^-31 of that largest one.
+ * Host checks: as pkv_paged_attention_prefill (head_dim 64 or 128, group 1, 2, 4 or
  * 8, block_size a power of two in [8, 1024], scale positive and finite), plus
  * mask_words >= 1 and 16-byte aligned per-token scale pools; pools of 2^31 or
  * more (block, KV head, token) rows are PKV_ERR_UNSUPPORTED. Device checks:

@@ -50,7 +50,7 @@
 // row's largest element and off by at most 2^-17 of it below), and S = hi K^T +
 // lo K^T in binary32 -- the tensor time of one 16-bit product, and no key is
 // converted. V's codes are widened exactly, to f16 with a scale per KV head, where
-// P is rounded to f16, and to bf16 with a scale per token, where a weight times its
+// P is rounded to f16 (kF16Lift), and to bf16 with a scale per token, where a weight times its
 // token's V scale is rounded to bf16 (whose range any scale fits). The softmax runs in base 2
 // with a reference maximum that moves only when a key exceeds it by 8; the normaliser
 // sums the weights in binary32 as they are before rounding.
@@ -84,6 +84,13 @@ using namespace tc;
 constexpr int kRows = 128;  // MMA M
 constexpr int kBN = 64;     // keys per tile
 constexpr float kLog2e = 1.4426950408889634f;
+// f16 weights are formed 2^7 larger: the reference maximum may lag by 2^8, so they stay
+// below 2^15, and those down to 2^-21 of the reference instead of 2^-14 are normal numbers.
+// Behind one key far above all others, the usual state of long contexts, the rest of the
+// row is such small weights; unlifted, a row of weights 2^-24 of its largest came out a
+// quarter off. The sums carry the same factor, and so it cancels. Below 2^-21 a weight's
+// error is at most 2^-32 of the reference's weight.
+constexpr float kF16Lift = 7.0f;
 
 template <int D, int MODE, int NT>
 struct Tree {
@@ -560,7 +567,8 @@ __device__ __forceinline__ bool softmax_tiles(const TreeArgs &a, const Unit &u, 
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: weights exp2(-inf) = 0
+                // nothing seen yet: weights exp2(-inf) = 0
+                const float ref = m == -INFINITY ? 0.0f : (kF16 ? kF16Lift : 0.0f) - m;
 #pragma unroll
                 for (int h = 0; h < W / 16; ++h) {
                     uint32_t w[8];

@@ -424,3 +424,39 @@ def test_maxima_that_grow_in_every_half_of_a_tile(d, drafts, cache):
     c["q"].copy_(q.bfloat16())
     for shares in (0, 1):
         check(c, shares=shares)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("gap", [20, 24])
+@pytest.mark.parametrize("n,drafts", [(32768, 4), (65536, 2), (2048, 36)])
+def test_one_key_far_above_a_long_flat_rest(n, drafts, gap, cache):
+    """One key's weight is 2^gap times every other's and its V is zero, so the small weights are the answer.
+    All of V is positive: errors of one sign add up. In one share (every weight next to the large one) and
+    in many."""
+    c = make([drafts], [n], 4, 1, 128, 256, cache, seed=51, words=2)
+    g = torch.Generator().manual_seed(52)
+    if cache == "fp8":
+        c["ks"].fill_(2.0 ** -6)
+        c["vs"].fill_(2.0 ** -8)
+    # queries of +-1 are exact in every operand type, so are the binary32 scores, nearly
+    q = torch.where(torch.rand(drafts, 4, 128, generator=g) < 0.5, -1.0, 1.0)
+    q[:, :, :64] = 1.0
+    c["q"].copy_(q.bfloat16())
+    k = 0.25 * torch.randn(n, 1, 128, generator=g)
+    k[5, :, :64] = gap * math.log(2) * math.sqrt(128) / 64
+    k[5, :, 64:] = 0
+    v = 0.5 + torch.rand(n, 1, 128, generator=g)
+    v[5] = 0
+    put(c, 0, 0, k, v)
+    ref, mag = reference(c)
+    assert float(mag.min()) > 0
+    for shares in (1, 0):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = call(c, shares=shares, dev_err=err)
+        assert K.read_device_error(err) == K.PKV_OK
+        # f16 weights below 2^-21 of the largest: each off by at most 2^-32 of it (a sum of at least 1), V at most 1.5 (1 + 2^-4)
+        small = 1.6 * n * 2.0 ** -32 if cache == "fp8" else 0.0
+        g64 = out.double().cpu()
+        tol = R.tree_tolerance(ref, mag, cache != "bf16", cache == "fp8_token") + small * (1 + R.U_BF16)
+        off = ((g64 - ref).abs() / tol)
+        assert bool((off <= 1).all()), f"{shares} shares: off by {float(off.max()):.3g} tolerances"

@@ -810,7 +810,9 @@ __device__ __forceinline__ float load_queries(const TreeArgs &a, const Unit &u, 
             sl2 *= fabsf(ks);
             if (ks < 0.0f) qs = -qs;
         }
-        if (!(amax <= 3.4e38f)) sl2 = __int_as_float(0x7FC00000);  // an infinite query: E4M3 has none
+        // an infinite query, which E4M3 has not, makes NaN of its row's operand: of every score then, but not of
+        // the row's scale, which enters behind the mask and would reach masked keys
+        if (!(amax <= 3.4e38f)) qs = __int_as_float(0x7FC00000);
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {  // 16 elements: one chunk of hi and of lo
             const uint4 v0 = live ? __ldg(qrow + 2 * c) : make_uint4(0, 0, 0, 0);

@@ -460,3 +460,24 @@ def test_one_key_far_above_a_long_flat_rest(n, drafts, gap, cache):
         tol = R.tree_tolerance(ref, mag, cache != "bf16", cache == "fp8_token") + small * (1 + R.U_BF16)
         off = ((g64 - ref).abs() / tol)
         assert bool((off <= 1).all()), f"{shares} shares: off by {float(off.max()):.3g} tolerances"
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("drafts", [6, 24, 40])
+def test_rows_that_see_nothing_are_zeros_whatever_their_query_holds(drafts, bad, cache):
+    """No token before the drafts and an empty mask row: zeros, even for a query that is not finite. The same
+    query where something is seen gives NaN, in its own row and head alone."""
+    c = make([drafts, drafts], [drafts, drafts], 8, 2, 128, 16, cache, seed=61, words=2)
+    c["mask"][2] = 0
+    clean = check(c)
+    for row in (2, drafts - 1, drafts + 3):
+        c["q"][row, 1, ::2] = bad
+        c["q"][row, 6] = bad
+    out = call(c)
+    hit = torch.zeros(2 * drafts, 8, dtype=torch.bool)
+    for row in (drafts - 1, drafts + 3):
+        hit[row, 1] = hit[row, 6] = True
+    assert bool((out[2] == 0).all())
+    assert bool(out.cpu()[hit].isnan().all())
+    assert torch.equal(out.cpu()[~hit], clean.cpu()[~hit])

@@ -88,9 +88,11 @@ constexpr int kBatch = 2;
 // 47.5 and 48.1 us instead of 43.1, 2777 into an E4M3 cache 18.3 and 22.5 instead of 16.
 constexpr int kMinBlocks = 5;
 
+// 16 bytes that the call does not read again. Not a read-only load: q_out may be q,
+// whose elements the thread that loaded them writes back.
 __device__ __forceinline__ uint4 load_row(const __nv_bfloat16 *p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;

@@ -210,3 +210,18 @@ def test_on_another_stream():
     got = call(c, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("N", [1, 64, 4001])
+def test_in_place_while_other_rows_are_loaded(N, style):
+    """q_out is q, in the fused projection: a token divided among warps, and more tokens than resident warps,
+    whose next loads are in flight while rows are written. The result is the one of a separate q_out, bit for bit."""
+    c = make(N, 32, 8, 128, 16, "bf16", seed=12)
+    want = call(c, style)
+    kp, vp = c["kp"].clone(), c["vp"].clone()
+    got = call(c, style, q_out=c["q"])
+    assert got is c["q"]
+    assert torch.equal(got.contiguous().view(torch.int16), want.view(torch.int16))
+    assert torch.equal(c["kp"].view(torch.int16), kp.view(torch.int16))
+    assert torch.equal(c["vp"].view(torch.int16), vp.view(torch.int16))

@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(256, PKV_ROPE_MIN_BLOCKS) store_kvcache_rope_k
         long long base;
         if (is_q) {
             base = (token * p.num_q_heads + r) * cpr;
-            a = __ldg(p.q + base + ca);
-            b = __ldg(p.q + base + cb);
+            a = p.q[base + ca];  // not a read-only load: q_out may be q
+            b = p.q[base + cb];
         } else {
             slot = __ldg(p.slots + token);
             base = (token * p.num_kv_heads + head) * cpr;

@@ -179,3 +179,22 @@ def test_decode_over_a_rotated_cache(dt, style):
                                        c.softmax_scale, hks, hvs, num_threads=THREADS)
     assert st == O.ORC_OK
     compare(out, ref, fp8, f"decode over rotated cache ({dt}, style {style})")
+
+
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("N", [1, 4001])
+def test_in_place_while_other_rows_are_loaded(N, style):
+    """q_out is q, with more rows than resident threads: the result is the one of a separate q_out, bit for bit."""
+    g = torch.Generator().manual_seed(77)
+    q = torch.randn(N, 32, 128, generator=g).bfloat16().cuda()
+    k, v = (torch.randn(N, 8, 128, generator=g).bfloat16().cuda() for _ in range(2))
+    shape = (-(-N // 16), 8, 16, 128)
+    pools = [torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    slots = torch.randperm(shape[0] * 16, generator=g)[:N].int().cuda()
+    pos = torch.randint(0, 300, (N,), generator=g).int().cuda()
+    cs = W.rope_cache(300, 128).cuda()
+    want = K.store_kvcache_rope(k, v, pools[0], pools[1], slots, pos, cs, q=q, style=style)
+    got = K.store_kvcache_rope(k, v, pools[2], pools[3], slots, pos, cs, q=q, q_out=q, style=style)
+    assert got is q and torch.equal(got.view(torch.int16), want.view(torch.int16))
+    for a, b in zip(pools[:2], pools[2:]):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))

@@ -470,7 +470,8 @@ PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int num_kv_heads, int h
  *  max_context_len  host-known bound on every context, at most
  *                 max_blocks_per_seq * block_size
  *  shares         into how many equal shares the work is cut, one thread block
- *                 each; 0: one or two per SM (fewer where the work is small). At most
+ *                 each; 0: one or two per SM of the current device, in the plan
+ *                 and in the call (fewer where the work is small). At most
  *                 4096. Sequences need not be alike: a share ends where it
  *                 ends, and partial results of what it cuts are joined
  *  workspace      device scratch of at least the plan's workspace_bytes,

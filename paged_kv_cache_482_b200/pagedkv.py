@@ -585,7 +585,8 @@ def tree_mask(parents, words=None):
 
 def plan_tree(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_context_len,
               cache_dtype=PKV_CACHE_BF16, shares=0) -> dict:
-    """The shares and workspace size of a ``paged_attention_tree`` call of these sizes."""
+    """The shares and workspace size of a ``paged_attention_tree`` call of these sizes. With ``shares`` 0 they
+    depend on the current device's number of SMs: plan with the device of the call current."""
     plan = _TreePlan()
     st = lib().pkv_plan_tree(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_context_len,
                              int(cache_dtype), shares, ctypes.byref(plan))
@@ -632,7 +633,12 @@ def paged_attention_tree(q, k_cache, v_cache, block_tables, cu_q_lens, context_l
     if out is None:
         out = _empty(q.shape, _BF16, index, stream)
     if workspace is None:
-        need = plan_tree(S, nq, nkv, d, bs, max_q_len, max_context_len, dt, shares)["workspace_bytes"]
+        sizes = (S, nq, nkv, d, bs, max_q_len, max_context_len, dt, shares)
+        if torch.cuda.current_device() == index:
+            need = plan_tree(*sizes)["workspace_bytes"]
+        else:  # the launch plans on the tensors' device
+            with torch.cuda.device(index):
+                need = plan_tree(*sizes)["workspace_bytes"]
         if need:
             workspace = _empty(need, _U8, index, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0

@@ -252,3 +252,35 @@ def test_tree_plan(K):
             K.plan_tree(*bad)
     assert K.lib().pkv_plan_tree(1, 32, 8, 128, 256, 8, 512, 0, 0, ctypes.POINTER(K._TreePlan)()) == \
         K.PKV_ERR_INVALID_ARG
+
+
+def test_tree_workspace_is_planned_on_the_tensors_device(K, monkeypatch):
+    """The number of shares follows the SMs of the device that is current: the workspace of a call on device 1
+    made while device 0 is current is planned with device 1 current, as the launch is."""
+    import contextlib
+
+    current, planned = [0], []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    def plan(*args):
+        planned.append((current[0], args))
+        return dict(shares=3, workspace_bytes=512)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(K, "_on_device", lambda *t: on)
+    monkeypatch.setattr(K, "_empty", lambda shape, dtype, index, stream: torch.empty(shape, dtype=dtype))
+    monkeypatch.setattr(K, "_run", lambda *a: None)
+    monkeypatch.setattr(K, "plan_tree", plan)
+    kc, vc = _pools()
+    i32 = dict(dtype=torch.int32)
+    for on in (1, 0):
+        K.paged_attention_tree(torch.zeros(3, 4, 64, dtype=torch.bfloat16), kc, vc, torch.zeros(2, 3, **i32),
+                               torch.zeros(3, **i32), torch.zeros(2, **i32), torch.zeros(3, 1, **i32), 0.1, 3)
+    assert [p[0] for p in planned] == [1, 0] and current == [0]
+    assert planned[0][1] == (2, 4, 2, 64, 16, 3, 48, K.PKV_CACHE_BF16, 0)

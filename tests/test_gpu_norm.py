@@ -82,3 +82,16 @@ def test_extremes():
     K.fused_add_rmsnorm(x, r, big.weight.cuda(), 1e-6)
     _, rref, _ = O.fused_add_rmsnorm(big.x, big.residual, big.weight, 1e-6)
     assert np.array_equal(bits(r), rref) and rref[0, 0] == 0x7F80
+
+
+@pytest.mark.parametrize("T,H", [(3, 4096), (8192, 1024)])
+def test_in_place_while_other_rows_are_loaded(T, H):
+    """out is x, with several rows per block, whose next loads are in flight while rows are written: the result
+    is the one of a separate out, bit for bit."""
+    wl = W.generate_norm(W.NormConfig("rows", T, H), 8)
+    x, r, w = wl.x.cuda(), wl.residual.cuda(), wl.weight.cuda()
+    r2 = r.clone()
+    want = K.fused_add_rmsnorm(x, r, w, 1e-6)
+    got = K.fused_add_rmsnorm(x, r2, w, 1e-6, out=x)
+    assert got.data_ptr() == x.data_ptr() and torch.equal(got.view(torch.int16), want.view(torch.int16))
+    assert torch.equal(r2.view(torch.int16), r.view(torch.int16))

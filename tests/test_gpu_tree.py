@@ -481,3 +481,82 @@ def test_rows_that_see_nothing_are_zeros_whatever_their_query_holds(drafts, bad,
     assert bool((out[2] == 0).all())
     assert bool(out.cpu()[hit].isnan().all())
     assert torch.equal(out.cpu()[~hit], clean.cpu()[~hit])
+
+
+def test_rows_of_lost_sequences_stay_and_the_others_are_right():
+    """cu_q_lens that descends or leaves the rows: the sequence's own rows are not written, the other
+    sequence's are as ever."""
+    for cu, ok, rows in (([0, 5, 3], 0, (0, 5)), ([-2, 3, 7], 1, (3, 7)), ([0, 3, 9], 0, (0, 3))):
+        c = make([3, 4], [40, 50], 8, 2, 128, 16, "bf16", seed=20)
+        c["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full_like(c["q"], 5.0)
+        call(c, out=out, dev_err=err, max_q_len=9)
+        assert K.read_device_error(err) == K.PKV_ERR_DEVICE_BOUNDS, cu
+        a, b = rows
+        assert bool((out[:a] == 5.0).all()) and bool((out[b:] == 5.0).all()), cu
+        one = dict(c, q=c["q"][a:b], mask=c["mask"][a:b], tab=c["tab"][ok:ok + 1], ctx=c["ctx"][ok:ok + 1],
+                   cu=torch.tensor([0, b - a], dtype=torch.int32))
+        ref, mag = reference(one)
+        close(c, out[a:b], ref, mag, str(cu))
+
+
+def test_a_causal_chain_equals_prefill_row_by_row():
+    """Both calls are within the tolerance of the formula, so within twice that of each other."""
+    c = make([20, 50], [333, 1000], 8, 2, 128, 16, "bf16", seed=25)
+    c["mask"] = torch.cat([K.tree_mask(list(range(-1, n - 1)), words=2)[0] for n in (20, 50)]).cuda()
+    out = call(c)
+    pre = K.paged_attention_prefill(c["q"], c["kp"], c["vp"], c["tab"], c["cu"], c["ctx"], c["scale"], c["most"])
+    ref, mag = reference(c)
+    tol = R.tree_tolerance(ref, mag, False, False)
+    assert bool(((out.double() - pre.double()).abs().cpu() <= 2 * tol).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("ql", [[4, 9, 1, 16, 12], [20, 32, 17, 5, 25]])
+@pytest.mark.parametrize("shares", [1, 2, 3, 10, 37, 300])
+def test_any_cut_of_units_of_one_row_tile(shares, ql, cache):
+    """As test_any_cut_of_the_work, with at most 128 rows: units of one copy of their rows and of two."""
+    c = make(ql, [2500, 70, 1, 1111, 180], 8, 2, 128, 16, cache, seed=11) if ql[2] == 1 else \
+        make(ql, [2500, 70, 40, 1111, 180], 8, 2, 128, 16, cache, seed=11)
+    p = K.plan_tree(5, 8, 2, 128, 16, c["most"], 2512, cache_dtype=K.cache_dtype(c["kp"], c["ks"]), shares=shares)
+    ws = torch.full((max(256, p["workspace_bytes"]),), 0xFF, dtype=torch.uint8, device="cuda")
+    check(c, shares=shares, workspace=ws)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("ql", [[12, 16], [12, 30]])
+@pytest.mark.parametrize("shares", [0, 1, 7])
+def test_what_is_masked_does_not_reach_a_row_of_one_row_tile(shares, ql, cache):
+    """As test_what_is_masked_does_not_reach_a_row, with units of one row tile and of two copies."""
+    c = make(ql, [50, 200], 8, 2, 128, 16, cache, seed=17)
+    clean = call(c, shares=shares).clone()
+    tab = c["tab"].cpu().long()
+    for seq, u in ((0, 3), (1, 7), (1, 11)):
+        t = int(c["ctx"][seq]) - ql[seq] + u
+        blk, off = int(tab[seq, t // 16]), t % 16
+        if cache == "bf16":
+            c["kp"][blk, :, off, 1] = float("nan")
+            c["vp"][blk, 0, off] = float("inf")
+            c["vp"][blk, 1, off, 5] = float("nan")
+        else:
+            c["kp"][blk, :, off, 1] = 0x7F
+            c["vp"][blk, 0, off] = 0x7F
+            c["vp"][blk, 1, off, 5] = 0x7F
+            if cache == "fp8_token":
+                c["vs"][blk, 1, off] = float("inf")
+    out = call(c, shares=shares)
+    saw = torch.zeros(sum(ql), dtype=torch.bool)
+    bits = R.sees(c["mask"], 32)
+    saw[:12] = bits[:12, 3]
+    saw[12:] = bits[12:, 7] | bits[12:, 11]
+    assert bool(saw.any()) and not bool(saw.all())
+    assert torch.equal(out.cpu()[~saw], clean.cpu()[~saw])
+    assert bool(out.cpu()[saw].isnan().any(-1).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_trees_that_are_small_against_the_bound(d, cache):
+    """max_q_len allows units of two row tiles, of which these trees fill a part of the first."""
+    check(make([8, 1, 5, 30, 3], [500, 60, 300, 1000, 3], 8, 2, d, 16, cache, seed=81, words=4), max_q_len=128)

@@ -175,7 +175,8 @@ PKV_API int pkv_store_kvcache_rope(const void *q, void *q_out, const void *k, co
  *  other arguments as pkv_store_kvcache_rope
  *
  * Slots of one call are distinct (apart from -1): of two rows for one slot
- * either may stay, and parts of both.
+ * either may stay, and parts of both. The sum of squares is accumulated in
+ * binary32, so rows with elements beyond about 1e18 in magnitude overflow it.
  *
  * Host checks: as pkv_store_kvcache_rope, plus strides that are multiples of
  * 8 elements and at least heads * head_dim, heads * head_dim at most 2^26, and
@@ -460,7 +461,9 @@ PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int num_kv_heads, int h
  * over t < base_i and over t = base_i + u for the u with bit u of the row's
  * mask set (the row itself only if its own bit is set). What a row does not
  * attend to does not reach it, infinities and NaN included; a row that sees
- * nothing (base_i = 0 and no bit) is zeros. Bits at and above c_i are ignored.
+ * nothing (base_i = 0 and no bit) is zeros, whatever its query holds, and so is
+ * one whose visible scores are all -inf. An infinity in the V of a draft that a
+ * row sees reaches it however small the weight. Bits at and above c_i are ignored.
  *
  *  q              [total_q][num_q_heads][head_dim] bf16, contiguous
  *  tree_mask      [total_q][mask_words] uint32: bit u % 32 of word u / 32

@@ -26,7 +26,8 @@
 //
 // Measured (B200): 8192 tokens, 32 query and 8 KV heads of 128, bf16: 43.1 us, 4.8
 // TB/s (a group of lanes per row, which reads the table for every head: 53 us);
-// 2777 tokens, 16 and 8 heads, per-token E4M3: 15.9 us; one token: 2.8 us.
+// into E4M3 with a scale per head 51.4 us; 2777 tokens, 16 and 8 heads, per-token E4M3:
+// 15.9 us; one token: 2.8 us.
 #include "pkv_common.cuh"
 #include "pkv_launch.h"
 #include "store_common.cuh"
